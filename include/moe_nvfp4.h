@@ -292,6 +292,130 @@ int moe_forward_arm(const moe_shape_t* shape);
  * MMA differs between the two arms. */
 moe_status_t moe_set_narrow_rows(int rows);
 
+/* ---------------------------------------------------------------------------------------------
+ * The block around the experts: the operators that a residual block with routed e4m3 experts is
+ * built from, each with the gradients of its floating inputs.  The experts' weights are codes
+ * that are made once, so the product's gradient is the one with respect to its rows (the same
+ * call with the transposed matrices).  The conventions at the top of this file hold; sizes that
+ * a call supports stand with it.  Calls with a `ws` record device-side errors in its first word
+ * (zero it once, read it with moe_get_device_status); the norms' workspace has no such word.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Tokens sorted by expert and back.  8 <= H <= 16384, H % 8 == 0; 1 <= E <= 1024; 1 <= k <= 16;
+ * T (k + 1) < 2^31; rows are bf16, or fp32 where fp32 = 1. */
+typedef struct {
+  int32_t T, H, E, k;
+  int32_t fp32;
+} moe_tokens_t;
+
+size_t moe_sort_workspace_size(int32_t T, int32_t E, int32_t k);   /* 0: unsupported sizes */
+
+/* Stable sort of the S = T k slots (slot s = t k + j) by expert, and the tokens' rows in that order.
+ *   x [T, H] rows; topk_ids int32 [T, k]: a negative id drops the slot (a padding token, a slot
+ *     over its expert's capacity); an id >= E drops it too and is recorded as MOE_ERR_INVALID_ARG
+ *   xs [S, H]: the slots' rows by expert, ascending slot id within an expert; the dropped slots'
+ *     rows follow, ascending, and hold zeros
+ *   offsets int32 [E + 1]: first row of each expert; offsets[E] = routed slots
+ *   sorted_slot int32 [S]: the slot of each row
+ *   slot_pos int32 [T, k]: the row p of each routed slot, -1 - p for a dropped one. */
+moe_status_t moe_sort_tokens(const void* x, const int32_t* topk_ids, const moe_tokens_t* shape, void* xs, int32_t* offsets,
+                             int32_t* sorted_slot, int32_t* slot_pos, void* ws, size_t ws_bytes, void* stream);
+
+/* dx[t] = sum over the routed slots of t of dxs[slot_pos], fp32 in rank order (0 without any). */
+moe_status_t moe_sort_tokens_backward(const void* dxs, const int32_t* slot_pos, const moe_tokens_t* shape, void* dx,
+                                      void* stream);
+
+/* out[t] = sum over the routed slots of t of topk_w[t, j] ys[slot_pos] (+ shared[t] when shared is
+ * not NULL), fp32 in rank order.  Rows and weights of dropped slots are not read. */
+moe_status_t moe_return_tokens(const void* ys, const int32_t* slot_pos, const float* topk_w, const void* shared,
+                               const moe_tokens_t* shape, void* out, void* stream);
+
+/* Gradient of moe_return_tokens: dys [S, H] (topk_w dout[t]; 0 in dropped slots' rows), dw fp32
+ * [T, k] (<dout[t], ys[slot_pos]>; 0 for dropped slots).  The shared rows' gradient is dout.
+ * slot_pos has to be moe_sort_tokens's (every row belongs to one slot). */
+moe_status_t moe_return_tokens_backward(const void* dout, const void* ys, const int32_t* slot_pos, const float* topk_w,
+                                        const moe_tokens_t* shape, void* dys, float* dw, void* stream);
+
+/* e4m3 matrices with one fp32 scale per 128 x 128 block: value = scales[g, n / 128, k / 128] *
+ * e4m3(codes[g, n, k]).  1 <= G <= 1025; 1 <= N <= 131072; 16 <= K <= 131072, K % 16 == 0 (the
+ * last block of a row or column may be partial). */
+typedef struct {
+  const uint8_t* codes;      /* [G, N, K] */
+  const float* scales;       /* [G, ceil(N / 128), ceil(K / 128)] */
+  int32_t G, N, K;
+} moe_block_fp8_weights_t;
+
+/* Load time: fp32 (w_is_fp32 = 1) or bf16 matrices [G, N, K] in that form, by the row rule of the
+ * FP8 arm taken over a block (amax 0 or not finite: scale 1; NaN keeps a NaN code, other values
+ * saturate at 448). */
+moe_status_t moe_quantize_block_fp8(const void* w, int w_is_fp32, int32_t G, int32_t N, int32_t K, uint8_t* codes,
+                                    float* scales, void* stream);
+
+/* Load time: the transposed matrices [G, K, N] (the same values; N % 16 == 0), with which
+ * moe_block_fp8_matmul gives the gradient with respect to the rows. */
+moe_status_t moe_transpose_block_fp8(const moe_block_fp8_weights_t* w, uint8_t* codes, float* scales, void* stream);
+
+/* bf16 rows [rows, K] in blocks of 1 x 128 under the same rule: codes [rows, 128 KB] (zero from K
+ * on), scales [rows, KB rounded up to 4] (zero from KB on), KB = ceil(K / 128). */
+moe_status_t moe_quantize_rows_block_fp8(const uint16_t* x, int64_t rows, int32_t K, uint8_t* codes, float* scales,
+                                         void* stream);
+
+size_t moe_block_fp8_workspace_size(int64_t M, int32_t K);   /* 0: unsupported sizes */
+
+/* out[m] = q(x[m]) W_g^T for the rows m of group g, with q the rows through
+ * moe_quantize_rows_block_fp8; fp32 accumulation, out [M, N] bf16 or fp32.
+ *   offsets int32 [G + 1]: group g has rows offsets[g] .. offsets[g + 1] (any may be empty); rows
+ *   from offsets[G] on are written as zeros.  NULL: one matrix (G = 1) for all rows.  Offsets that
+ *   do not start at 0, decrease or pass M are recorded as MOE_ERR_INVALID_ARG; out is then zeros. */
+moe_status_t moe_block_fp8_matmul(const uint16_t* x, int64_t M, const int32_t* offsets, const moe_block_fp8_weights_t* w,
+                                  void* out, int out_is_fp32, void* ws, size_t ws_bytes, void* stream);
+
+/* Norms before and after a block.  rms(v) = v rstd, rstd = 1 / sqrt(mean(v^2) + eps), per row;
+ * a weight vector w stands for w + weight_offset.  8 <= H <= 16384, H % 8 == 0; T < 2^31.
+ * Tensors: the residual stream (x, out, dout, dx, dresidual) is bf16, or fp32 where residual_fp32;
+ * the block's output (y, dy) is bf16, or fp32 where branch_fp32; normed rows (n, dn) are bf16;
+ * weights, their gradients and rstd are fp32. */
+enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1,      /* fp32 [H] */
+  MOE_GATE_TOKEN = 2,        /* fp32 [T] */
+  MOE_GATE_ELEMENT = 3       /* bf16 [T, H] */
+};
+typedef struct {
+  int32_t T, H;
+  int32_t residual_fp32, branch_fp32;
+  int32_t gate;              /* MOE_GATE_*; moe_norm_before and its gradient ignore it */
+  float eps, weight_offset;  /* eps >= 0 */
+  float residual_scale, branch_scale;
+} moe_norm_t;
+
+size_t moe_norm_workspace_size(int32_t T, int32_t H);   /* of the gradients; 0: unsupported sizes */
+
+/* n = rms(x) weight; rstd [T] may be NULL. */
+moe_status_t moe_norm_before(const void* x, const float* weight, const moe_norm_t* shape, uint16_t* n, float* rstd,
+                             void* stream);
+
+/* dx = gradient through the norm (+ dresidual when not NULL: the gradient that reaches x past
+ * the block), dweight [H] = sum over tokens.  rstd is moe_norm_before's. */
+moe_status_t moe_norm_before_backward(const uint16_t* dn, const void* x, const float* weight, const float* rstd,
+                                      const void* dresidual, const moe_norm_t* shape, void* dx, float* dweight, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/* out = residual_scale x + branch_scale gate (rms(y) weight), and with weight_next the next block's
+ * n = rms(out) weight_next of the stored (rounded) out, the same as moe_norm_before(out).
+ * gate is NULL for MOE_GATE_NONE; n is given exactly when weight_next is; rstd and rstd_next may
+ * be NULL.  out may be x. */
+moe_status_t moe_norm_after(const void* y, const void* x, const float* weight, const void* gate, const float* weight_next,
+                            const moe_norm_t* shape, void* out, uint16_t* n, float* rstd, float* rstd_next, void* stream);
+
+/* Gradient of moe_norm_after.  dn, out (the stored output), weight_next, rstd_next and dweight_next
+ * belong to the fused next norm and are all NULL without it; gate and dgate (the gate's type and
+ * shape) are NULL for MOE_GATE_NONE.  Column sums are taken in a fixed order. */
+moe_status_t moe_norm_after_backward(const void* dout, const uint16_t* dn, const void* y, const void* out,
+                                     const float* weight, const void* gate, const float* weight_next, const float* rstd,
+                                     const float* rstd_next, const moe_norm_t* shape, void* dy, void* dx, float* dweight,
+                                     void* dgate, float* dweight_next, void* ws, size_t ws_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* moe_status_string(moe_status_t status);
 

@@ -96,6 +96,7 @@ def _declare(L):
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
         fn.argtypes, fn.restype = args, res
+    block.declare(L)
 
 
 def _check(fn: str, status: int):
@@ -365,3 +366,8 @@ __all__ = ["Shape", "NVFP4Weights", "MoeError", "load", "workspace_size", "works
            "forward", "forward_profiled", "forward_arm", "router_logits", "forward_routed", "FP8Weights",
            "prepare_fp8", "quantize_rows_e4m3", "forward_fp8", "ARM_NAMES", "device_status", "status_string",
            "set_narrow_rows", "DECODE_MAX_T", "LIB_PATH"]
+
+from . import block  # noqa: E402  (uses the helpers above)
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += block.__all__

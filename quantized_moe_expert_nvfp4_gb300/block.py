@@ -1,0 +1,336 @@
+"""Binding of the operators around the routed experts: tokens sorted by expert and back, the e4m3
+product with a scale per block of 128, and the norms before and after a block, with their gradients.
+
+Argument marshalling only, in the manner of the package: types, shapes, devices and contiguity are
+checked here, everything else by the C ABI of `include/moe_nvfp4.h`, which documents each call.
+Outputs may be passed in; those that are not are allocated.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import MoeError, _check, _ptr, _stream, load
+
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = 0, 1, 2, 3
+
+
+class MoeTokens(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("fp32", ctypes.c_int32)]
+
+
+class MoeBlockFp8Weights(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("G", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32)]
+
+
+class MoeNorm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("residual_fp32", ctypes.c_int32),
+                ("branch_fp32", ctypes.c_int32), ("gate", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float)]
+
+
+def declare(L):
+    P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    TK, W8, NM = ctypes.POINTER(MoeTokens), ctypes.POINTER(MoeBlockFp8Weights), ctypes.POINTER(MoeNorm)
+    sigs = {
+        "moe_sort_workspace_size": ([I32, I32, I32], SZ),
+        "moe_sort_tokens": ([P, P, TK, P, P, P, P, P, SZ, P], I32),
+        "moe_sort_tokens_backward": ([P, P, TK, P, P], I32),
+        "moe_return_tokens": ([P, P, P, P, TK, P, P], I32),
+        "moe_return_tokens_backward": ([P, P, P, P, TK, P, P, P], I32),
+        "moe_quantize_block_fp8": ([P, I32, I32, I32, I32, P, P, P], I32),
+        "moe_transpose_block_fp8": ([W8, P, P, P], I32),
+        "moe_quantize_rows_block_fp8": ([P, I64, I32, P, P, P], I32),
+        "moe_block_fp8_workspace_size": ([I64, I32], SZ),
+        "moe_block_fp8_matmul": ([P, I64, P, W8, P, I32, P, SZ, P], I32),
+        "moe_norm_workspace_size": ([I32, I32], SZ),
+        "moe_norm_before": ([P, P, NM, P, P, P], I32),
+        "moe_norm_before_backward": ([P, P, P, P, P, NM, P, P, P, SZ, P], I32),
+        "moe_norm_after": ([P, P, P, P, P, NM, P, P, P, P, P], I32),
+        "moe_norm_after_backward": ([P, P, P, P, P, P, P, P, P, NM, P, P, P, P, P, P, SZ, P], I32),
+    }
+    for name, (args, res) in sigs.items():
+        fn = getattr(L, name)
+        fn.argtypes, fn.restype = args, res
+
+
+def _row_type(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.bfloat16:
+        return 0
+    if t.dtype == torch.float32:
+        return 1
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def _shaped(t: torch.Tensor | None, shape: tuple, name: str) -> None:
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _out(t: torch.Tensor | None, shape: tuple, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _shaped(t, shape, name)
+    return t
+
+
+def _ws(fn: str, nbytes: int, device) -> torch.Tensor:
+    if nbytes == 0:
+        raise MoeError(fn, -2)
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+# ------------------------------------------------------------------ tokens by expert and back
+
+def sort_workspace(T: int, E: int, k: int, device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for sort_tokens of up to T tokens (its first word is the device status)."""
+    return _ws("moe_sort_workspace_size", load().moe_sort_workspace_size(T, E, k), device)
+
+
+def sort_tokens(x, topk_ids, E: int, ws, xs=None, offsets=None, sorted_slot=None, slot_pos=None, stream=None):
+    """Rows of x [T, H] (bf16 or fp32) by expert: (xs [T k, H], offsets [E + 1], sorted_slot [T k],
+    slot_pos [T, k]).  Slots with a negative id are dropped: their rows come last and are zeros, and
+    their slot_pos is -1 - row."""
+    T, H = x.shape
+    k = topk_ids.shape[1]
+    _shaped(topk_ids, (T, k), "topk_ids")
+    S = T * k
+    fp32 = _row_type(x, "x")
+    i32 = torch.int32
+    xs = _out(xs, (S, H), x.dtype, x, "xs")
+    offsets = _out(offsets, (E + 1,), i32, x, "offsets")
+    sorted_slot = _out(sorted_slot, (S,), i32, x, "sorted_slot")
+    slot_pos = _out(slot_pos, (T, k), i32, x, "slot_pos")
+    _check("moe_sort_tokens", load().moe_sort_tokens(
+        _ptr(x), _ptr(topk_ids, i32, "topk_ids"), MoeTokens(T, H, E, k, fp32), _ptr(xs, x.dtype, "xs"),
+        _ptr(offsets, i32, "offsets"), _ptr(sorted_slot, i32, "sorted_slot"), _ptr(slot_pos, i32, "slot_pos"),
+        _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+    return xs, offsets, sorted_slot, slot_pos
+
+
+def _slots(rows, slot_pos, name):
+    T, k = slot_pos.shape
+    H = rows.shape[1]
+    _shaped(rows, (T * k, H), name)
+    return T, k, H, MoeTokens(T, H, 1, k, _row_type(rows, name))
+
+
+def sort_tokens_backward(dxs, slot_pos, dx=None, stream=None):
+    """dx [T, H]: for each token the sum of its routed slots' rows of dxs [T k, H]."""
+    T, k, H, shape = _slots(dxs, slot_pos, "dxs")
+    dx = _out(dx, (T, H), dxs.dtype, dxs, "dx")
+    _check("moe_sort_tokens_backward", load().moe_sort_tokens_backward(
+        _ptr(dxs), _ptr(slot_pos, torch.int32, "slot_pos"), shape, _ptr(dx, dxs.dtype, "dx"), _stream(stream)))
+    return dx
+
+
+def return_tokens(ys, slot_pos, topk_w, shared=None, out=None, stream=None):
+    """out [T, H]: for each token the weighted sum of its routed slots' rows of ys [T k, H], plus its
+    row of `shared` [T, H] when given."""
+    T, k, H, shape = _slots(ys, slot_pos, "ys")
+    _shaped(topk_w, (T, k), "topk_w")
+    _shaped(shared, (T, H), "shared")
+    out = _out(out, (T, H), ys.dtype, ys, "out")
+    _check("moe_return_tokens", load().moe_return_tokens(
+        _ptr(ys), _ptr(slot_pos, torch.int32, "slot_pos"), _ptr(topk_w, torch.float32, "topk_w"),
+        _ptr(shared, ys.dtype, "shared"), shape, _ptr(out, ys.dtype, "out"), _stream(stream)))
+    return out
+
+
+def return_tokens_backward(dout, ys, slot_pos, topk_w, dys=None, dw=None, stream=None):
+    """Gradients (dys [T k, H], dw fp32 [T, k]) of return_tokens; that of `shared` is dout itself."""
+    T, k, H, shape = _slots(ys, slot_pos, "ys")
+    _shaped(dout, (T, H), "dout")
+    _shaped(topk_w, (T, k), "topk_w")
+    dys = _out(dys, (T * k, H), ys.dtype, ys, "dys")
+    dw = _out(dw, (T, k), torch.float32, ys, "dw")
+    _check("moe_return_tokens_backward", load().moe_return_tokens_backward(
+        _ptr(dout, ys.dtype, "dout"), _ptr(ys), _ptr(slot_pos, torch.int32, "slot_pos"),
+        _ptr(topk_w, torch.float32, "topk_w"), shape, _ptr(dys, ys.dtype, "dys"), _ptr(dw, torch.float32, "dw"),
+        _stream(stream)))
+    return dys, dw
+
+
+# ------------------------------------------------------------------ e4m3 with a scale per block of 128
+
+@dataclass
+class BlockFP8Weights:
+    """Matrices in e4m3 with a scale per 128 x 128 block: codes u8 [G, N, K], scales fp32
+    [G, ceil(N / 128), ceil(K / 128)]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    def c(self) -> MoeBlockFp8Weights:
+        G, N, K = self.codes.shape
+        _shaped(self.scales, (G, -(-N // 128), -(-K // 128)), "scales")
+        return MoeBlockFp8Weights(_ptr(self.codes, torch.uint8, "codes"), _ptr(self.scales, torch.float32, "scales"), G, N, K)
+
+
+def quantize_block_fp8(w: torch.Tensor, stream=None) -> BlockFP8Weights:
+    """Load-time quantization of fp32 or bf16 matrices [G, N, K]."""
+    G, N, K = w.shape
+    codes = torch.empty(G, N, K, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(G, -(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
+    _check("moe_quantize_block_fp8", load().moe_quantize_block_fp8(
+        _ptr(w), _row_type(w, "w"), G, N, K, _ptr(codes), _ptr(scales), _stream(stream)))
+    return BlockFP8Weights(codes, scales)
+
+
+def transpose_block_fp8(w: BlockFP8Weights, stream=None) -> BlockFP8Weights:
+    """The transposed matrices [G, K, N] (the same values), for the gradient of the product."""
+    G, N, K = w.codes.shape
+    t = BlockFP8Weights(torch.empty(G, K, N, dtype=torch.uint8, device=w.codes.device),
+                        torch.empty(G, -(-K // 128), -(-N // 128), dtype=torch.float32, device=w.codes.device))
+    _check("moe_transpose_block_fp8", load().moe_transpose_block_fp8(w.c(), _ptr(t.codes), _ptr(t.scales), _stream(stream)))
+    return t
+
+
+def quantize_rows_block_fp8(x: torch.Tensor, stream=None):
+    """bf16 [rows, K] -> (codes u8 [rows, 128 KB], scales fp32 [rows, KB rounded up to 4]), KB = ceil(K / 128)."""
+    rows, K = x.shape
+    KB = -(-K // 128)
+    codes = torch.empty(rows, 128 * KB, dtype=torch.uint8, device=x.device)
+    scales = torch.empty(rows, -(-KB // 4) * 4, dtype=torch.float32, device=x.device)
+    _check("moe_quantize_rows_block_fp8", load().moe_quantize_rows_block_fp8(
+        _ptr(x, torch.bfloat16, "x"), rows, K, _ptr(codes), _ptr(scales), _stream(stream)))
+    return codes, scales
+
+
+def block_fp8_workspace(M: int, w: BlockFP8Weights, device=None) -> torch.Tensor:
+    """A zero-filled workspace for block_fp8_matmul of up to M rows (its first word is the device status)."""
+    return _ws("moe_block_fp8_workspace_size", load().moe_block_fp8_workspace_size(M, w.codes.shape[2]),
+               device if device is not None else w.codes.device)
+
+
+def block_fp8_matmul(x, w: BlockFP8Weights, ws, offsets=None, out=None, out_fp32: bool = False, stream=None):
+    """x bf16 [M, K] quantized in blocks of 128 times the matrices: out [M, N] bf16 or fp32 (the type
+    of `out`, when given).  offsets int32 [G + 1] (sort_tokens's): rows of each matrix; rows past the
+    last are zeros.  Without offsets, one matrix (G = 1) for all rows."""
+    M, K = x.shape
+    G, N, wk = w.codes.shape
+    if K != wk:
+        raise ValueError(f"x has {K} columns, the matrices {wk}")
+    _shaped(offsets, (G + 1,), "offsets")
+    if out is None:
+        out = torch.empty(M, N, dtype=torch.float32 if out_fp32 else torch.bfloat16, device=x.device)
+    _shaped(out, (M, N), "out")
+    _check("moe_block_fp8_matmul", load().moe_block_fp8_matmul(
+        _ptr(x, torch.bfloat16, "x"), M, _ptr(offsets, torch.int32, "offsets"), w.c(), _ptr(out), _row_type(out, "out"),
+        _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+    return out
+
+
+# ------------------------------------------------------------------ norms before and after a block
+
+def norm_workspace(T: int, H: int, device="cuda") -> torch.Tensor:
+    """Workspace of the norms' gradients for up to T tokens."""
+    return _ws("moe_norm_workspace_size", load().moe_norm_workspace_size(T, H), device)
+
+
+def _gate(gate, T, H):
+    """(MOE_GATE_*, its type) of a gate: fp32 [H] or [T], or bf16 [T, H].  A 1-D gate of H == T elements
+    is per channel; pass [T, 1] for one per token."""
+    if gate is None:
+        return GATE_NONE, None
+    shape = tuple(gate.shape)
+    if shape == (H,):
+        return GATE_CHANNEL, torch.float32
+    if shape in ((T,), (T, 1)):
+        return GATE_TOKEN, torch.float32
+    if shape == (T, H):
+        return GATE_ELEMENT, torch.bfloat16
+    raise ValueError(f"gate must have shape ({H},), ({T},), ({T}, 1) or ({T}, {H}), got {shape}")
+
+
+def norm_before(x, weight, eps: float = 1e-6, weight_offset: float = 0.0, n=None, rstd=None, stream=None):
+    """(n bf16 [T, H], rstd fp32 [T]) of x [T, H] (bf16 or fp32): n = x rstd (weight + weight_offset)."""
+    T, H = x.shape
+    _shaped(weight, (H,), "weight")
+    n = _out(n, (T, H), torch.bfloat16, x, "n")
+    rstd = _out(rstd, (T,), torch.float32, x, "rstd")
+    _check("moe_norm_before", load().moe_norm_before(
+        _ptr(x), _ptr(weight, torch.float32, "weight"),
+        MoeNorm(T, H, _row_type(x, "x"), 0, GATE_NONE, eps, weight_offset, 1.0, 1.0), _ptr(n, torch.bfloat16, "n"),
+        _ptr(rstd, torch.float32, "rstd"), _stream(stream)))
+    return n, rstd
+
+
+def norm_before_backward(dn, x, weight, rstd, ws, dresidual=None, weight_offset: float = 0.0, dx=None, dw=None, stream=None):
+    """(dx, dw) of norm_before; dresidual (x's type) is added to dx."""
+    T, H = x.shape
+    for t, shape, name in ((dn, (T, H), "dn"), (weight, (H,), "weight"), (rstd, (T,), "rstd"), (dresidual, (T, H), "dresidual")):
+        _shaped(t, shape, name)
+    f32 = torch.float32
+    dx = _out(dx, (T, H), x.dtype, x, "dx")
+    dw = _out(dw, (H,), f32, x, "dw")
+    _check("moe_norm_before_backward", load().moe_norm_before_backward(
+        _ptr(dn, torch.bfloat16, "dn"), _ptr(x), _ptr(weight, f32, "weight"), _ptr(rstd, f32, "rstd"),
+        _ptr(dresidual, x.dtype, "dresidual"), MoeNorm(T, H, _row_type(x, "x"), 0, GATE_NONE, 0.0, weight_offset, 1.0, 1.0),
+        _ptr(dx, x.dtype, "dx"), _ptr(dw, f32, "dw"), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+    return dx, dw
+
+
+def norm_after(y, x, weight, gate=None, w_next=None, residual_scale: float = 1.0, branch_scale: float = 1.0,
+               eps: float = 1e-6, weight_offset: float = 0.0, out=None, n=None, rstd=None, rstd_next=None, stream=None):
+    """out = residual_scale x + branch_scale gate (rms(y) weight), and with w_next the next block's norm
+    n of the stored out: (out, n or None, rstd, rstd_next or None)."""
+    T, H = x.shape
+    kind, gate_type = _gate(gate, T, H)
+    for t, shape, name in ((y, (T, H), "y"), (weight, (H,), "weight"), (w_next, (H,), "w_next")):
+        _shaped(t, shape, name)
+    f32 = torch.float32
+    out = _out(out, (T, H), x.dtype, x, "out")
+    rstd = _out(rstd, (T,), f32, x, "rstd")
+    if w_next is not None:
+        n = _out(n, (T, H), torch.bfloat16, x, "n")
+        rstd_next = _out(rstd_next, (T,), f32, x, "rstd_next")
+    elif n is not None or rstd_next is not None:
+        raise ValueError("n and rstd_next are outputs of the next norm: they need w_next")
+    _check("moe_norm_after", load().moe_norm_after(
+        _ptr(y), _ptr(x), _ptr(weight, f32, "weight"), _ptr(gate, gate_type, "gate"), _ptr(w_next, f32, "w_next"),
+        MoeNorm(T, H, _row_type(x, "x"), _row_type(y, "y"), kind, eps, weight_offset, residual_scale, branch_scale),
+        _ptr(out, x.dtype, "out"), _ptr(n, torch.bfloat16, "n"), _ptr(rstd, f32, "rstd"), _ptr(rstd_next, f32, "rstd_next"),
+        _stream(stream)))
+    return out, n, rstd, rstd_next
+
+
+def norm_after_backward(dout, y, weight, rstd, ws, gate=None, dn=None, out=None, w_next=None, rstd_next=None,
+                        residual_scale: float = 1.0, branch_scale: float = 1.0, weight_offset: float = 0.0, dy=None, dx=None,
+                        dw=None, dgate=None, dw_next=None, stream=None):
+    """(dy, dx, dw, dgate or None, dw_next or None) of norm_after.  With the fused next norm, dn is the
+    gradient of its output and `out` the stored output of the forward call."""
+    T, H = y.shape
+    kind, gate_type = _gate(gate, T, H)
+    nexts = (dn, out, w_next, rstd_next)
+    if any(t is None for t in nexts) and any(t is not None for t in nexts):
+        raise ValueError("dn, out, w_next and rstd_next belong to the next norm: give all of them or none")
+    for t, shape, name in ((dout, (T, H), "dout"), (weight, (H,), "weight"), (rstd, (T,), "rstd"), (dn, (T, H), "dn"),
+                           (out, (T, H), "out"), (w_next, (H,), "w_next"), (rstd_next, (T,), "rstd_next")):
+        _shaped(t, shape, name)
+    f32 = torch.float32
+    dy = _out(dy, (T, H), y.dtype, y, "dy")
+    dx = _out(dx, (T, H), dout.dtype, dout, "dx")
+    dw = _out(dw, (H,), f32, y, "dw")
+    if gate is not None:
+        dgate = _out(dgate, tuple(gate.shape), gate_type, y, "dgate")
+    if w_next is not None:
+        dw_next = _out(dw_next, (H,), f32, y, "dw_next")
+    if (gate is None and dgate is not None) or (w_next is None and dw_next is not None):
+        raise ValueError("dgate needs gate, dw_next needs w_next")
+    _check("moe_norm_after_backward", load().moe_norm_after_backward(
+        _ptr(dout), _ptr(dn, torch.bfloat16, "dn"), _ptr(y), _ptr(out, dout.dtype, "out"), _ptr(weight, f32, "weight"),
+        _ptr(gate, gate_type, "gate"), _ptr(w_next, f32, "w_next"), _ptr(rstd, f32, "rstd"), _ptr(rstd_next, f32, "rstd_next"),
+        MoeNorm(T, H, _row_type(dout, "dout"), _row_type(y, "y"), kind, 0.0, weight_offset, residual_scale, branch_scale),
+        _ptr(dy, y.dtype, "dy"), _ptr(dx, dout.dtype, "dx"), _ptr(dw, f32, "dw"), _ptr(dgate, gate_type, "dgate"),
+        _ptr(dw_next, f32, "dw_next"), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+    return dy, dx, dw, dgate, dw_next
+
+
+__all__ = ["sort_workspace", "sort_tokens", "sort_tokens_backward", "return_tokens", "return_tokens_backward",
+           "BlockFP8Weights", "quantize_block_fp8", "transpose_block_fp8", "quantize_rows_block_fp8", "block_fp8_workspace",
+           "block_fp8_matmul", "norm_workspace", "norm_before", "norm_before_backward", "norm_after", "norm_after_backward",
+           "GATE_NONE", "GATE_CHANNEL", "GATE_TOKEN", "GATE_ELEMENT"]

@@ -8,11 +8,12 @@
 #include "internal.cuh"
 
 namespace moe {
-namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+namespace {
 
 moe_status_t check_shape(const moe_shape_t* s) {
   if (!s) return MOE_ERR_INVALID_ARG;
@@ -57,6 +58,8 @@ moe_status_t check_arch() {
   return ok ? MOE_OK : MOE_ERR_ARCH;
 }
 
+}  // namespace
+
 // The current device must be compute capability 10.3 and `stream` must belong to it (a stream
 // created on another device would run the launches there, against pointers of this one).  The
 // legacy and per-thread default stream handles always name the current device.  A stream that
@@ -77,6 +80,8 @@ moe_status_t check_device(void* stream) {
 }
 
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+namespace {
 
 struct Ws {
   int32_t* status;

@@ -1,0 +1,291 @@
+// C ABI of the operators around the routed experts: tokens sorted by expert and back, the e4m3
+// product with a scale per block of 128, and the norms before and after a block.  Argument checks
+// and workspace layout; host code only.
+#include <cmath>
+
+#include "group_tiles.cuh"
+#include "internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxRowElems = 16384;
+constexpr int kMaxMatrixDim = 1 << 17;
+constexpr size_t kStatusBytes = 256;
+
+bool aligned16_or_null(const void* p) { return !p || aligned16(p); }
+bool flag(int32_t v) { return v == 0 || v == 1; }
+
+moe_status_t check_ws_bytes(const void* ws, size_t have, size_t need) {
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_INVALID_ARG;
+  return have < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
+
+moe_status_t check_tokens(const moe_tokens_t* s) {
+  if (!s || !flag(s->fp32)) return MOE_ERR_INVALID_ARG;
+  if (s->T < 0 || s->H < 8 || s->H > kMaxRowElems || s->H % 8 || s->E < 1 || s->E > kMaxE || s->k < 1 || s->k > kMaxK)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<int64_t>(s->T) * (s->k + 1) >= (int64_t{1} << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+SortShape sort_shape(const moe_tokens_t& s) { return {s.T, s.H, s.E, s.k, s.fp32 != 0}; }
+
+struct SortWs {
+  size_t hist, totals, total;
+};
+SortWs sort_ws(int64_t S, int E) {
+  SortWs w;
+  w.hist = kStatusBytes;
+  w.totals = align256(w.hist + sizeof(int32_t) * static_cast<size_t>(sort_chunks(S)) * (E + 1));
+  w.total = align256(w.totals + sizeof(int32_t) * static_cast<size_t>(E + 1));
+  return w;
+}
+
+moe_status_t check_block_weights(const moe_block_fp8_weights_t* w) {
+  if (!w || !aligned16(w->codes) || !aligned16(w->scales)) return MOE_ERR_INVALID_ARG;
+  if (w->G < 1 || w->G > kMaxGroups || w->N < 1 || w->N > kMaxMatrixDim || w->K < 16 || w->K > kMaxMatrixDim || w->K % 16)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+
+struct BlockFp8Ws {
+  size_t codes, scales, total;
+};
+BlockFp8Ws block_fp8_ws(int64_t M, int K) {
+  const int64_t KB = blocks_of(K);
+  BlockFp8Ws w;
+  w.codes = kStatusBytes;
+  w.scales = align256(w.codes + static_cast<size_t>(M) * KB * 128);
+  w.total = align256(w.scales + sizeof(float) * static_cast<size_t>(M) * ((KB + 3) & ~int64_t{3}));
+  return w;
+}
+
+moe_status_t check_norm(const moe_norm_t* s) {
+  if (!s || !flag(s->residual_fp32) || !flag(s->branch_fp32) || s->gate < MOE_GATE_NONE || s->gate > MOE_GATE_ELEMENT)
+    return MOE_ERR_INVALID_ARG;
+  if (!(s->eps >= 0.0f) || !std::isfinite(s->eps) || !std::isfinite(s->weight_offset) ||
+      !std::isfinite(s->residual_scale) || !std::isfinite(s->branch_scale))
+    return MOE_ERR_INVALID_ARG;
+  if (s->T < 0 || s->H < 8 || s->H > kMaxRowElems || s->H % 8) return MOE_ERR_UNSUPPORTED_SHAPE;
+  return MOE_OK;
+}
+
+size_t norm_ws_bytes(int64_t T, int H) { return align256(sizeof(float) * 3 * static_cast<size_t>(norm_max_parts(T, H)) * H); }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_sort_workspace_size(int32_t T, int32_t E, int32_t k) {
+  const moe_tokens_t s = {T, 8, E, k, 0};
+  if (check_tokens(&s) != MOE_OK) return 0;
+  return sort_ws(static_cast<int64_t>(T) * k, E).total;
+}
+
+moe_status_t moe_sort_tokens(const void* x, const int32_t* topk_ids, const moe_tokens_t* shape, void* xs, int32_t* offsets,
+                             int32_t* sorted_slot, int32_t* slot_pos, void* ws, size_t ws_bytes, void* stream) {
+  moe_status_t st = check_tokens(shape);
+  if (st != MOE_OK) return st;
+  if (!aligned16(offsets)) return MOE_ERR_INVALID_ARG;
+  if (shape->T > 0 && (!aligned16(x) || !aligned16(topk_ids) || !aligned16(xs) || !aligned16(sorted_slot) || !aligned16(slot_pos)))
+    return MOE_ERR_INVALID_ARG;
+  const SortWs L = sort_ws(static_cast<int64_t>(shape->T) * shape->k, shape->E);
+  if ((st = check_ws_bytes(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (shape->T == 0) return cuda_status(cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (shape->E + 1), cs));
+  char* b = static_cast<char*>(ws);
+  return cuda_status(launch_sort_tokens(sort_shape(*shape), x, topk_ids, xs, offsets, sorted_slot, slot_pos,
+                                        reinterpret_cast<int32_t*>(b + L.hist), reinterpret_cast<int32_t*>(b + L.totals),
+                                        reinterpret_cast<int32_t*>(b), cs));
+}
+
+moe_status_t moe_sort_tokens_backward(const void* dxs, const int32_t* slot_pos, const moe_tokens_t* shape, void* dx,
+                                      void* stream) {
+  moe_status_t st = check_tokens(shape);
+  if (st != MOE_OK) return st;
+  if (shape->T == 0) return MOE_OK;
+  if (!aligned16(dxs) || !aligned16(slot_pos) || !aligned16(dx)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  return cuda_status(launch_return_tokens(sort_shape(*shape), dxs, slot_pos, nullptr, nullptr, dx,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_return_tokens(const void* ys, const int32_t* slot_pos, const float* topk_w, const void* shared,
+                               const moe_tokens_t* shape, void* out, void* stream) {
+  moe_status_t st = check_tokens(shape);
+  if (st != MOE_OK) return st;
+  if (shape->T == 0) return MOE_OK;
+  if (!aligned16(ys) || !aligned16(slot_pos) || !aligned16(topk_w) || !aligned16_or_null(shared) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  return cuda_status(launch_return_tokens(sort_shape(*shape), ys, slot_pos, topk_w, shared, out,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_return_tokens_backward(const void* dout, const void* ys, const int32_t* slot_pos, const float* topk_w,
+                                        const moe_tokens_t* shape, void* dys, float* dw, void* stream) {
+  moe_status_t st = check_tokens(shape);
+  if (st != MOE_OK) return st;
+  if (shape->T == 0) return MOE_OK;
+  if (!aligned16(dout) || !aligned16(ys) || !aligned16(slot_pos) || !aligned16(topk_w) || !aligned16(dys) || !aligned16(dw))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  return cuda_status(launch_return_tokens_grad(sort_shape(*shape), dout, ys, slot_pos, topk_w, dys, dw,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_quantize_block_fp8(const void* w, int w_is_fp32, int32_t G, int32_t N, int32_t K, uint8_t* codes,
+                                    float* scales, void* stream) {
+  const moe_block_fp8_weights_t q = {codes, scales, G, N, K};
+  moe_status_t st = check_block_weights(&q);
+  if (st != MOE_OK) return st;
+  if (!aligned16(w) || !flag(w_is_fp32)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  return cuda_status(launch_quantize_blocks(w, w_is_fp32 != 0, G, N, K, codes, scales, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_transpose_block_fp8(const moe_block_fp8_weights_t* w, uint8_t* codes, float* scales, void* stream) {
+  moe_status_t st = check_block_weights(w);
+  if (st != MOE_OK) return st;
+  if (w->N % 16) return MOE_ERR_UNSUPPORTED_SHAPE;   // the transposed rows have N elements
+  if (!aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  return cuda_status(launch_transpose_blocks(w->codes, w->scales, w->G, w->N, w->K, codes, scales,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_quantize_rows_block_fp8(const uint16_t* x, int64_t rows, int32_t K, uint8_t* codes, float* scales,
+                                         void* stream) {
+  if (rows < 0 || rows >= (int64_t{1} << 31) || K < 16 || K > kMaxMatrixDim || K % 16) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0) return MOE_OK;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  moe_status_t st = check_device(stream);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_quantize_rows_block(x, rows, K, codes, scales, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_block_fp8_workspace_size(int64_t M, int32_t K) {
+  if (M < 0 || M >= (int64_t{1} << 31) || K < 16 || K > kMaxMatrixDim || K % 16) return 0;
+  return block_fp8_ws(M, K).total;
+}
+
+moe_status_t moe_block_fp8_matmul(const uint16_t* x, int64_t M, const int32_t* offsets, const moe_block_fp8_weights_t* w,
+                                  void* out, int out_is_fp32, void* ws, size_t ws_bytes, void* stream) {
+  moe_status_t st = check_block_weights(w);
+  if (st != MOE_OK) return st;
+  if (M < 0 || M >= (int64_t{1} << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!flag(out_is_fp32) || !aligned16_or_null(offsets) || (!offsets && w->G != 1)) return MOE_ERR_INVALID_ARG;
+  if (M > 0 && (!aligned16(x) || !aligned16(out))) return MOE_ERR_INVALID_ARG;
+  const BlockFp8Ws L = block_fp8_ws(M, w->K);
+  if ((st = check_ws_bytes(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  if (M == 0) return MOE_OK;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  char* b = static_cast<char*>(ws);
+  BlockFp8Args a;
+  a.x_codes = reinterpret_cast<const uint8_t*>(b + L.codes);
+  a.x_scales = reinterpret_cast<const float*>(b + L.scales);
+  a.w_codes = w->codes;
+  a.w_scales = w->scales;
+  a.offsets = offsets;
+  a.M = static_cast<int>(M);
+  a.N = w->N;
+  a.K = w->K;
+  a.G = w->G;
+  a.out = out;
+  a.out_fp32 = out_is_fp32 != 0;
+  a.status = reinterpret_cast<int32_t*>(b);
+  cudaError_t e = launch_quantize_rows_block(x, M, w->K, reinterpret_cast<uint8_t*>(b + L.codes),
+                                             reinterpret_cast<float*>(b + L.scales), cs);
+  if (e == cudaSuccess) e = launch_block_fp8_matmul(a, cs);
+  return cuda_status(e);
+}
+
+size_t moe_norm_workspace_size(int32_t T, int32_t H) {
+  const moe_norm_t s = {T, H, 0, 0, MOE_GATE_NONE, 0.0f, 0.0f, 0.0f, 0.0f};
+  if (check_norm(&s) != MOE_OK) return 0;
+  return norm_ws_bytes(T, H);
+}
+
+moe_status_t moe_norm_before(const void* x, const float* weight, const moe_norm_t* shape, uint16_t* n, float* rstd,
+                             void* stream) {
+  moe_status_t st = check_norm(shape);
+  if (st != MOE_OK) return st;
+  if (shape->T == 0) return MOE_OK;
+  if (!aligned16(x) || !aligned16(weight) || !aligned16(n) || !aligned16_or_null(rstd)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  return cuda_status(launch_norm_before(*shape, x, weight, n, rstd, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_norm_before_backward(const uint16_t* dn, const void* x, const float* weight, const float* rstd,
+                                      const void* dresidual, const moe_norm_t* shape, void* dx, float* dweight, void* ws,
+                                      size_t ws_bytes, void* stream) {
+  moe_status_t st = check_norm(shape);
+  if (st != MOE_OK) return st;
+  if (!aligned16(weight) || !aligned16(dweight)) return MOE_ERR_INVALID_ARG;
+  if (shape->T > 0 && (!aligned16(dn) || !aligned16(x) || !aligned16(rstd) || !aligned16_or_null(dresidual) || !aligned16(dx)))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws_bytes(ws, ws_bytes, norm_ws_bytes(shape->T, shape->H))) != MOE_OK) return st;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (shape->T == 0) return cuda_status(cudaMemsetAsync(dweight, 0, sizeof(float) * shape->H, cs));
+  return cuda_status(launch_norm_before_grad(*shape, dn, x, weight, rstd, dresidual, dx, dweight, static_cast<float*>(ws), cs));
+}
+
+moe_status_t moe_norm_after(const void* y, const void* x, const float* weight, const void* gate, const float* weight_next,
+                            const moe_norm_t* shape, void* out, uint16_t* n, float* rstd, float* rstd_next, void* stream) {
+  moe_status_t st = check_norm(shape);
+  if (st != MOE_OK) return st;
+  if ((gate != nullptr) != (shape->gate != MOE_GATE_NONE) && shape->T > 0) return MOE_ERR_INVALID_ARG;
+  if (shape->T == 0) return MOE_OK;
+  if (!aligned16(y) || !aligned16(x) || !aligned16(weight) || !aligned16_or_null(gate) || !aligned16_or_null(weight_next) ||
+      !aligned16(out) || !aligned16_or_null(n) || !aligned16_or_null(rstd) || !aligned16_or_null(rstd_next))
+    return MOE_ERR_INVALID_ARG;
+  if ((weight_next != nullptr) != (n != nullptr) || (rstd_next && !n)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  return cuda_status(launch_norm_after(*shape, y, x, weight, gate, weight_next, out, n, rstd, rstd_next,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_norm_after_backward(const void* dout, const uint16_t* dn, const void* y, const void* out,
+                                     const float* weight, const void* gate, const float* weight_next, const float* rstd,
+                                     const float* rstd_next, const moe_norm_t* shape, void* dy, void* dx, float* dweight,
+                                     void* dgate, float* dweight_next, void* ws, size_t ws_bytes, void* stream) {
+  moe_status_t st = check_norm(shape);
+  if (st != MOE_OK) return st;
+  const bool next = weight_next != nullptr;
+  const bool gated = shape->gate != MOE_GATE_NONE;
+  if (!aligned16(weight) || !aligned16(dweight) || !aligned16_or_null(weight_next) || !aligned16_or_null(dweight_next) ||
+      !aligned16_or_null(gate) || !aligned16_or_null(dgate))
+    return MOE_ERR_INVALID_ARG;
+  if (next != (dweight_next != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (shape->T > 0) {
+    if (!aligned16(dout) || !aligned16(y) || !aligned16(rstd) || !aligned16(dy) || !aligned16(dx)) return MOE_ERR_INVALID_ARG;
+    if (gated != (gate != nullptr) || gated != (dgate != nullptr)) return MOE_ERR_INVALID_ARG;
+    if (next && (!aligned16(dn) || !aligned16(out) || !aligned16(rstd_next))) return MOE_ERR_INVALID_ARG;
+    if (!next && (dn || rstd_next)) return MOE_ERR_INVALID_ARG;
+  } else if (shape->gate == MOE_GATE_CHANNEL && !dgate) {
+    return MOE_ERR_INVALID_ARG;
+  }
+  if ((st = check_ws_bytes(ws, ws_bytes, norm_ws_bytes(shape->T, shape->H))) != MOE_OK) return st;
+  if ((st = check_device(stream)) != MOE_OK) return st;
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (shape->T == 0) {   // sums over no tokens
+    const size_t bytes = sizeof(float) * shape->H;
+    cudaError_t e = cudaMemsetAsync(dweight, 0, bytes, cs);
+    if (e == cudaSuccess && next) e = cudaMemsetAsync(dweight_next, 0, bytes, cs);
+    if (e == cudaSuccess && shape->gate == MOE_GATE_CHANNEL) e = cudaMemsetAsync(dgate, 0, bytes, cs);
+    return cuda_status(e);
+  }
+  return cuda_status(launch_norm_after_grad(*shape, dout, dn, y, out, weight, gate, weight_next, rstd, rstd_next, dy, dx,
+                                            dweight, dgate, dweight_next, static_cast<float*>(ws), cs));
+}
+
+}  // extern "C"

@@ -1,0 +1,175 @@
+// Operands of the e4m3 product with one fp32 scale per block of 128: rows of activations in
+// blocks of 1 x 128, weights in blocks of 128 x 128.  Both follow the row rule of the FP8 arm on
+// a block instead of a row:
+//   amax = max |v| over the block, inv = 448 / amax, scale = amax / 448 (IEEE fp32 divisions;
+//   amax 0 or not finite: both 1), code = e4m3 nearest even, saturating, of the fp32 product
+//   v inv; the value is scale * e4m3(code).
+// Every step is one IEEE operation, so the codes are reproducible bit for bit.
+#include <algorithm>
+
+#include "internal.cuh"
+
+namespace moe {
+namespace {
+
+__device__ __forceinline__ void block_rule(float amax, float& inv, float& scale) {
+  const bool usable = amax > 0.0f && amax <= 3.402823466e38f;
+  inv = usable ? __fdiv_rn(448.0f, amax) : 1.0f;
+  scale = usable ? __fdiv_rn(amax, 448.0f) : 1.0f;
+}
+
+// max that keeps a NaN (fmaxf drops it), so that a block with one is recognised as not finite
+__device__ __forceinline__ float max_nan(float a, float b) { return a != a ? a : (b != b ? b : fmaxf(a, b)); }
+
+__device__ __forceinline__ uint32_t codes2(float a, float b, float inv) {
+  const float2 q = make_float2(__fmul_rn(a, inv), __fmul_rn(b, inv));
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3));
+}
+
+// One warp per row: 16 lanes hold a block (eight bf16 each).  codes [rows, 128 KB], zero from K
+// on; scales [rows, KB rounded up to 4], zero from KB on (KB = blocks of a row).
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restrict__ x, int64_t rows, int K, int KB,
+                                                            uint2* __restrict__ codes, float* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  pdl_wait();
+  if (r >= rows) return;
+  const int units = K / 8, pitch = (KB + 3) & ~3;
+  const uint4* src = x + r * units;
+  uint2* dst = codes + r * KB * 16;
+  for (int kb0 = 0; kb0 < pitch; kb0 += 32) {   // 32 scales are written together
+    float mine = 0.0f;
+#pragma unroll 4
+    for (int b = 0; b < 32; b += 2) {
+      const int kb = kb0 + b + (lane >> 4);
+      if (kb0 + b >= KB) break;
+      const int u = kb * 16 + (lane & 15);
+      const uint4 q = u < units ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      float v[8], amax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(v[i]));
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+      float inv, scale;
+      block_rule(amax, inv, scale);
+      if (kb < KB)
+        dst[u] = make_uint2(codes2(v[0], v[1], inv) | (codes2(v[2], v[3], inv) << 16),
+                            codes2(v[4], v[5], inv) | (codes2(v[6], v[7], inv) << 16));
+      // lane b of the 32 keeps the scale of block kb0 + b, lane b + 1 that of the next
+      const float s0 = __shfl_sync(0xffffffffu, scale, 0), s1 = __shfl_sync(0xffffffffu, scale, 16);
+      if (lane == b) mine = s0;
+      if (lane == b + 1 && kb0 + b + 1 < KB) mine = s1;
+    }
+    if (kb0 + lane < pitch) scales[r * pitch + kb0 + lane] = mine;
+  }
+}
+
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load4(const uint16_t* p) {
+  const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u), __uint_as_float(q.y << 16),
+                     __uint_as_float(q.y & 0xffff0000u));
+}
+
+// One CTA per 128 x 128 block (load time): the block's amax, then its codes.
+template <typename V>
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(const V* __restrict__ w, int N, int K,
+                                                              uint32_t* __restrict__ codes, float* __restrict__ scales) {
+  __shared__ float s_max[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int KB = gridDim.x, NB = (N + 127) / 128;
+  const int kb = blockIdx.x, nb = blockIdx.y;
+  const int64_t g = blockIdx.z;
+  const int k = kb * 128 + lane * 4;
+  const int64_t base = g * N * K;
+  pdl_wait();
+  float amax = 0.0f;
+  for (int r = warp; r < 128; r += 8) {
+    const int n = nb * 128 + r;
+    if (n < N && k < K) {
+      const float4 v = load4(w + base + static_cast<int64_t>(n) * K + k);
+      amax = max_nan(max_nan(max_nan(fabsf(v.x), fabsf(v.y)), max_nan(fabsf(v.z), fabsf(v.w))), amax);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+  if (lane == 0) s_max[warp] = amax;
+  __syncthreads();
+  amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max_nan(amax, s_max[i]);
+  float inv, scale;
+  block_rule(amax, inv, scale);
+  if (threadIdx.x == 0) scales[(g * NB + nb) * KB + kb] = scale;
+  for (int r = warp; r < 128; r += 8) {
+    const int n = nb * 128 + r;
+    if (n < N && k < K) {
+      const int64_t at = base + static_cast<int64_t>(n) * K + k;
+      const float4 v = load4(w + at);
+      codes[at / 4] = codes2(v.x, v.y, inv) | (codes2(v.z, v.w, inv) << 16);
+    }
+  }
+}
+
+// One CTA per 128 x 128 block (load time): the block and its scale in the transposed matrix.
+__global__ void __launch_bounds__(256) transpose_blocks_kernel(const uint32_t* __restrict__ codes,
+                                                               const float* __restrict__ scales, int N, int K,
+                                                               uint32_t* __restrict__ t_codes, float* __restrict__ t_scales) {
+  __shared__ uint8_t s[128][132];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int KB = gridDim.x, NB = gridDim.y;
+  const int kb = blockIdx.x, nb = blockIdx.y;
+  const int64_t g = blockIdx.z, base = g * N * K;
+  pdl_wait();
+  for (int r = warp; r < 128; r += 8) {
+    const int n = nb * 128 + r, k = kb * 128 + lane * 4;
+    uint32_t q = 0;
+    if (n < N && k < K) q = __ldg(codes + (base + static_cast<int64_t>(n) * K + k) / 4);
+    *reinterpret_cast<uint32_t*>(&s[r][lane * 4]) = q;
+  }
+  __syncthreads();
+  for (int r = warp; r < 128; r += 8) {
+    const int k = kb * 128 + r, n = nb * 128 + lane * 4;
+    if (k < K && n < N) {
+      uint32_t q = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q |= static_cast<uint32_t>(s[lane * 4 + i][r]) << (8 * i);
+      t_codes[(base + static_cast<int64_t>(k) * N + n) / 4] = q;
+    }
+  }
+  if (threadIdx.x == 0) t_scales[(g * KB + kb) * NB + nb] = __ldg(scales + (g * NB + nb) * KB + kb);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_rows_block(const uint16_t* x, int64_t rows, int K, uint8_t* codes, float* scales,
+                                       cudaStream_t st) {
+  const int64_t blocks = (rows * 32 + 255) / 256;
+  return launch_pdl(true, quantize_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
+                    reinterpret_cast<const uint4*>(x), rows, K, (K + 127) / 128, reinterpret_cast<uint2*>(codes), scales);
+}
+
+cudaError_t launch_quantize_blocks(const void* w, bool fp32, int G, int N, int K, uint8_t* codes, float* scales,
+                                   cudaStream_t st) {
+  const dim3 grid((K + 127) / 128, (N + 127) / 128, G);
+  uint32_t* c = reinterpret_cast<uint32_t*>(codes);
+  if (fp32)
+    return launch_pdl(true, quantize_blocks_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(w), N, K, c,
+                      scales);
+  return launch_pdl(true, quantize_blocks_kernel<uint16_t>, grid, dim3(256), 0, st, static_cast<const uint16_t*>(w), N, K,
+                    c, scales);
+}
+
+cudaError_t launch_transpose_blocks(const uint8_t* codes, const float* scales, int G, int N, int K, uint8_t* t_codes,
+                                    float* t_scales, cudaStream_t st) {
+  return launch_pdl(true, transpose_blocks_kernel, dim3((K + 127) / 128, (N + 127) / 128, G), dim3(256), 0, st,
+                    reinterpret_cast<const uint32_t*>(codes), scales, N, K, reinterpret_cast<uint32_t*>(t_codes), t_scales);
+}
+
+}  // namespace moe

@@ -322,6 +322,60 @@ cudaError_t launch_router_simt(const uint16_t* x, const moe_nvfp4_weights_t& w, 
 // Work list of a one-group GEMM over rows [0, rows) in items of tile_rows (meta[0] = count).
 cudaError_t launch_dense_tiles(int rows, int tile_rows, int4* tiles, int32_t* meta, cudaStream_t st);
 
+// ------------------------------------------------------------------ the block around the experts
+// Host checks shared by the C entry points (abi.cu).
+size_t align256(size_t x);
+bool aligned16(const void* p);
+moe_status_t check_device(void* stream);
+moe_status_t cuda_status(cudaError_t e);
+
+// Tokens sorted by expert and back (token_sort.cu); rows of H elements, H e % 16 == 0 bytes.
+struct SortShape {
+  int T, H, E, k;
+  bool fp32;
+};
+int64_t sort_chunks(int64_t S);   // rows of hist [chunks, E + 1]
+cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t* ids, void* xs, int32_t* offsets,
+                               int32_t* sorted_slot, int32_t* slot_pos, int32_t* hist, int32_t* totals, int32_t* status,
+                               cudaStream_t st);
+// w NULL: weights 1; shared NULL: none.
+cudaError_t launch_return_tokens(const SortShape& s, const void* rows, const int32_t* slot_pos, const float* w,
+                                 const void* shared, void* out, cudaStream_t st);
+cudaError_t launch_return_tokens_grad(const SortShape& s, const void* dout, const void* ys, const int32_t* slot_pos,
+                                      const float* w, void* dys, float* dw, cudaStream_t st);
+
+// e4m3 with a scale per block of 128 (block_fp8.cu, gemm_block_fp8.cu).
+cudaError_t launch_quantize_rows_block(const uint16_t* x, int64_t rows, int K, uint8_t* codes, float* scales,
+                                       cudaStream_t st);
+cudaError_t launch_quantize_blocks(const void* w, bool fp32, int G, int N, int K, uint8_t* codes, float* scales,
+                                   cudaStream_t st);
+cudaError_t launch_transpose_blocks(const uint8_t* codes, const float* scales, int G, int N, int K, uint8_t* t_codes,
+                                    float* t_scales, cudaStream_t st);
+struct BlockFp8Args {
+  const uint8_t* x_codes;       // [M, 128 KB], KB = ceil(K / 128)
+  const float* x_scales;        // [M, KB rounded up to 4]
+  const uint8_t* w_codes;       // [G, N, K]
+  const float* w_scales;        // [G, ceil(N / 128), KB]
+  const int32_t* offsets;       // [G + 1], or NULL: one group of all rows
+  int M, N, K, G;
+  void* out;                    // [M, N] bf16 or fp32
+  bool out_fp32;
+  int32_t* status;
+};
+cudaError_t launch_block_fp8_matmul(const BlockFp8Args& a, cudaStream_t st);
+
+// Norms before and after a block (block_norm.cu); part: [3][norm_max_parts][H] fp32.
+int64_t norm_max_parts(int64_t T, int H);
+cudaError_t launch_norm_before(const moe_norm_t& s, const void* x, const float* w, void* n, float* rstd, cudaStream_t st);
+cudaError_t launch_norm_before_grad(const moe_norm_t& s, const void* dn, const void* x, const float* w, const float* rstd,
+                                    const void* dres, void* dx, float* dw, float* part, cudaStream_t st);
+cudaError_t launch_norm_after(const moe_norm_t& s, const void* y, const void* x, const float* w, const void* gate,
+                              const float* w_next, void* out, void* n, float* rstd, float* rstd_next, cudaStream_t st);
+cudaError_t launch_norm_after_grad(const moe_norm_t& s, const void* dout, const void* dn, const void* y, const void* out,
+                                   const float* w, const void* gate, const float* w_next, const float* rstd,
+                                   const float* rstd_next, void* dy, void* dx, float* dw, void* dgate, float* dw_next,
+                                   float* part, cudaStream_t st);
+
 cudaError_t launch_quantize(const float* w, int64_t G, int64_t N, int64_t K, uint8_t* packed,
                             uint8_t* scales, float* scale2, cudaStream_t st);
 

@@ -1,0 +1,421 @@
+// Tokens sorted by expert and back, with the routing weights applied, and the gradients of both.
+//
+// Slot s = t k + j is rank j of token t, with expert id[s]; an id outside [0, E) drops the slot.
+// The stable sort of the slots by key (the expert, or E for a dropped slot) is a permutation p of
+// all S = T k slots: routed rows first, grouped by expert, then the dropped slots' rows, which
+// hold zeros.  slot_pos[s] = p(s), written as -1 - p(s) for a dropped slot, is all that the other
+// three calls need:
+//   sort     xs[p(s)] = x[t]                        sort'    dx[t] = sum_j dxs[p(s)]
+//   return   out[t] = sum_j w[s] ys[p(s)]           return'  dys[p(s)] = w[s] dout[t],
+//                                                            dw[s] = <dout[t], ys[p(s)]>
+// with sums over the routed ranks only, in fp32 and in rank order (no atomics: the same bits on
+// every call).  All four move S rows once and T rows once and are bound by HBM.
+#include <algorithm>
+
+#include "internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = 1024;                 // slots per CTA of the counting and placing kernels
+constexpr int kPerWarp = kChunk / kWarps;
+
+__device__ __forceinline__ int key_of(int id, int E) { return static_cast<unsigned>(id) < static_cast<unsigned>(E) ? id : E; }
+
+// ------------------------------------------------------------------ one launch (small batches)
+// One CTA per token.  A slot's position is the number of slots that sort before it, counted by a
+// warp over all S keys in shared memory: S k compares per CTA and no dependence between CTAs.
+__global__ void __launch_bounds__(kThreads) sort_rank_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ ids,
+                                                             int T, int units, int E, int k, uint4* __restrict__ xs,
+                                                             int32_t* __restrict__ offsets,
+                                                             int32_t* __restrict__ sorted_slot,
+                                                             int32_t* __restrict__ slot_pos, int32_t* status) {
+  extern __shared__ int s_key[];
+  __shared__ int s_pos[kMaxK];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int S = T * k, t = blockIdx.x;
+  pdl_wait();
+  for (int i = threadIdx.x; i < S; i += kThreads) {
+    const int id = ids[i];
+    if (id >= E && t == 0) report_device_error(status, kDevBadIndex);
+    s_key[i] = key_of(id, E);
+  }
+  const uint4* row = x + static_cast<int64_t>(t) * units;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < units) v = __ldg(row + threadIdx.x);   // in flight while the ranks are counted
+  __syncthreads();
+  for (int j = warp; j < k; j += kWarps) {
+    const int s = t * k + j, key = s_key[s];
+    int c = 0;
+    for (int i = lane; i < S; i += 32) c += (s_key[i] < key || (s_key[i] == key && i < s)) ? 1 : 0;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) {
+      s_pos[j] = key < E ? c : -1 - c;
+      slot_pos[s] = s_pos[j];
+      sorted_slot[c] = s;
+    }
+  }
+  for (int e = t * kWarps + warp; e <= E; e += gridDim.x * kWarps) {
+    int c = 0;
+    for (int i = lane; i < S; i += 32) c += s_key[i] < e ? 1 : 0;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) offsets[e] = c;
+  }
+  __syncthreads();
+  for (int u = threadIdx.x; u < units; u += kThreads) {
+    if (u >= kThreads) v = __ldg(row + u);
+    for (int j = 0; j < k; ++j) {
+      const int p = s_pos[j];
+      xs[static_cast<int64_t>(p >= 0 ? p : -1 - p) * units + u] = p >= 0 ? v : make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ counting sort (any batch)
+// hist[c][key]: slots of chunk c with that key.
+__global__ void __launch_bounds__(kThreads) sort_count_kernel(const int32_t* __restrict__ ids, int S, int E,
+                                                              int32_t* __restrict__ hist, int32_t* status) {
+  __shared__ int s_cnt[kMaxE + 1];
+  pdl_wait_then_release();
+  for (int e = threadIdx.x; e <= E; e += kThreads) s_cnt[e] = 0;
+  __syncthreads();
+  const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kChunk;
+#pragma unroll
+  for (int i = 0; i < kChunk / kThreads; ++i) {
+    const int64_t s = s0 + i * kThreads + threadIdx.x;
+    if (s < S) {
+      const int id = __ldg(ids + s);
+      if (id >= E) report_device_error(status, kDevBadIndex);
+      atomicAdd(&s_cnt[key_of(id, E)], 1);
+    }
+  }
+  __syncthreads();
+  int32_t* h = hist + static_cast<int64_t>(blockIdx.x) * (E + 1);
+  for (int e = threadIdx.x; e <= E; e += kThreads) h[e] = s_cnt[e];
+}
+
+// Column-wise exclusive prefix of hist over the chunks, in place, and the columns' totals: 32 keys
+// per CTA, 32 threads per key, each over a contiguous run of chunks.
+__global__ void __launch_bounds__(1024) sort_scan_kernel(int32_t* __restrict__ hist, int chunks, int E,
+                                                         int32_t* __restrict__ totals) {
+  __shared__ int s_sum[32][33];
+  pdl_wait_then_release();
+  const int c = threadIdx.x & 31, seg = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + c;
+  const int per = (chunks + 31) / 32;
+  const int a = min(chunks, seg * per), b = min(chunks, a + per);
+  int sum = 0;
+  if (e <= E)
+    for (int i = a; i < b; ++i) sum += hist[static_cast<int64_t>(i) * (E + 1) + e];
+  s_sum[c][seg] = sum;
+  __syncthreads();
+  {   // warp `seg` scans key `seg` of the CTA over the 32 runs
+    const int v = s_sum[seg][c];
+    int incl = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (c >= d) incl += o;
+    }
+    s_sum[seg][c] = incl - v;
+    if (c == 31 && blockIdx.x * 32 + seg <= E) totals[blockIdx.x * 32 + seg] = incl;
+  }
+  __syncthreads();
+  if (e <= E) {
+    int run = s_sum[c][seg];
+    for (int i = a; i < b; ++i) {
+      int32_t* h = hist + static_cast<int64_t>(i) * (E + 1) + e;
+      const int v = *h;
+      *h = run;
+      run += v;
+    }
+  }
+}
+
+// Places one chunk's slots: every warp counts its run of the chunk, each key's cursor is split
+// into per-warp cursors in run order, and each warp places its run 32 slots at a time (equal keys
+// of a group in lane order).
+__global__ void __launch_bounds__(kThreads) sort_place_kernel(const int32_t* __restrict__ ids, int S, int E,
+                                                              const int32_t* __restrict__ hist,
+                                                              const int32_t* __restrict__ totals,
+                                                              int32_t* __restrict__ offsets,
+                                                              int32_t* __restrict__ sorted_slot,
+                                                              int32_t* __restrict__ slot_pos) {
+  extern __shared__ int s_cur[];               // [kWarps][E + 1]
+  __shared__ int s_wsum[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = E + 1;
+  for (int i = threadIdx.x; i < kWarps * n; i += kThreads) s_cur[i] = 0;
+  pdl_wait();
+  __syncthreads();
+  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * kChunk + warp * kPerWarp;
+  int key[kPerWarp / 32];
+#pragma unroll
+  for (int i = 0; i < kPerWarp / 32; ++i) {
+    const int64_t s = w0 + i * 32 + lane;
+    key[i] = s < S ? key_of(__ldg(ids + s), E) : -1;
+    if (key[i] >= 0) atomicAdd(&s_cur[warp * n + key[i]], 1);
+  }
+  // exclusive prefix of the totals: a run of keys per thread
+  const int per = (n + kThreads - 1) / kThreads;
+  const int e0 = threadIdx.x * per, e1 = min(n, e0 + per);
+  int sum = 0;
+  for (int e = e0; e < e1; ++e) sum += __ldg(totals + e);
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) s_wsum[warp] = incl;
+  __syncthreads();
+  int run = incl - sum;
+  for (int w = 0; w < warp; ++w) run += s_wsum[w];
+  const int32_t* base = hist + static_cast<int64_t>(blockIdx.x) * n;
+  for (int e = e0; e < e1; ++e) {
+    if (blockIdx.x == 0) offsets[e] = run;     // offsets[E] = the routed slots
+    int cur = run + __ldg(base + e);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int c = s_cur[w * n + e];
+      s_cur[w * n + e] = cur;
+      cur += c;
+    }
+    run += __ldg(totals + e);
+  }
+  __syncthreads();
+  int* cur = s_cur + warp * n;
+#pragma unroll
+  for (int i = 0; i < kPerWarp / 32; ++i) {
+    const int64_t s = w0 + i * 32 + lane;
+    const unsigned same = __match_any_sync(0xffffffffu, key[i]);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    const int p = key[i] >= 0 ? cur[key[i]] + rank : 0;
+    __syncwarp();
+    if (key[i] >= 0 && rank == 0) cur[key[i]] += __popc(same);
+    __syncwarp();
+    if (key[i] >= 0) {
+      slot_pos[s] = key[i] < E ? p : -1 - p;
+      sorted_slot[p] = static_cast<int32_t>(s);
+    }
+  }
+}
+
+// xs rows of one token per CTA: its x row is read once and written to its k places.
+__global__ void __launch_bounds__(kThreads) sort_gather_kernel(const uint4* __restrict__ x,
+                                                               const int32_t* __restrict__ slot_pos, int units, int k,
+                                                               uint4* __restrict__ xs) {
+  __shared__ int s_pos[kMaxK];
+  const int64_t t = blockIdx.x;
+  const uint4* row = x + t * units;
+  pdl_wait();
+  if (threadIdx.x < k) s_pos[threadIdx.x] = __ldg(slot_pos + t * k + threadIdx.x);
+  __syncthreads();
+  for (int u = threadIdx.x; u < units; u += blockDim.x) {
+    const uint4 v = __ldg(row + u);
+    for (int j = 0; j < k; ++j) {
+      const int p = s_pos[j];
+      xs[static_cast<int64_t>(p >= 0 ? p : -1 - p) * units + u] = p >= 0 ? v : make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ rows back to tokens
+template <typename V>
+struct Elems;                                  // a 16-byte unit as fp32 values
+template <>
+struct Elems<uint16_t> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ void get(const uint4& q, float (&f)[n]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 put(const float (&f)[n]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Elems<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ void get(const uint4& q, float (&f)[n]) {
+    f[0] = __uint_as_float(q.x);
+    f[1] = __uint_as_float(q.y);
+    f[2] = __uint_as_float(q.z);
+    f[3] = __uint_as_float(q.w);
+  }
+  static __device__ __forceinline__ uint4 put(const float (&f)[n]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+// A row position as read from the caller's slot_pos: a routed row in [0, S), or -1 for a dropped
+// slot or (reported) for anything else.  `place` is the row the slot owns, routed or dropped.
+__device__ __forceinline__ int routed_row(int p, int64_t S, int32_t* status) {
+  if (p < 0) return -1;
+  if (p >= S) {
+    if (status) report_device_error(status, kDevBadIndex);
+    return -1;
+  }
+  return p;
+}
+
+// out[t] = sum_j w[t, j] rows[p] (+ shared[t]); w == NULL: weights 1 (the gradient of the sort).
+// One thread per (token, 16-byte unit); the loads of up to four ranks are issued together.
+template <typename V>
+__global__ void __launch_bounds__(kThreads) return_kernel(const uint4* __restrict__ rows,
+                                                          const int32_t* __restrict__ slot_pos,
+                                                          const float* __restrict__ w, const uint4* __restrict__ shared,
+                                                          int64_t T, int units, int k, uint4* __restrict__ out) {
+  constexpr int n = Elems<V>::n;
+  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  pdl_wait();
+  if (idx >= T * units) return;
+  const int64_t t = idx / units;
+  const int u = static_cast<int>(idx - t * units);
+  const int64_t S = T * k;
+  float acc[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) acc[i] = 0.0f;
+  for (int j0 = 0; j0 < k; j0 += 4) {
+    uint4 q[4];
+    float wj[4];
+    bool take[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      take[i] = false;
+      if (j0 + i < k) {
+        const int p = routed_row(__ldg(slot_pos + t * k + j0 + i), S, nullptr);
+        take[i] = p >= 0;
+        wj[i] = w ? __ldg(w + t * k + j0 + i) : 1.0f;
+        if (take[i]) q[i] = __ldg(rows + static_cast<int64_t>(p) * units + u);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (take[i]) {
+        float f[n];
+        Elems<V>::get(q[i], f);
+#pragma unroll
+        for (int c = 0; c < n; ++c) acc[c] = fmaf(wj[i], f[c], acc[c]);
+      }
+    }
+  }
+  if (shared) {
+    float f[n];
+    Elems<V>::get(__ldg(shared + idx), f);
+#pragma unroll
+    for (int c = 0; c < n; ++c) acc[c] += f[c];
+  }
+  out[idx] = Elems<V>::put(acc);
+}
+
+// The gradient of the weighted return, one CTA per token: for each rank the row w dout[t] (zeros
+// for a dropped slot) and the dot product of dout[t] with the rank's row.
+template <typename V>
+__global__ void __launch_bounds__(kThreads) return_grad_kernel(const uint4* __restrict__ dout,
+                                                               const uint4* __restrict__ ys,
+                                                               const int32_t* __restrict__ slot_pos,
+                                                               const float* __restrict__ w, int64_t T, int units, int k,
+                                                               uint4* __restrict__ dys, float* __restrict__ dw) {
+  constexpr int n = Elems<V>::n;
+  __shared__ float s_dot[kMaxK][kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x, S = T * k;
+  pdl_wait();
+  for (int j = 0; j < k; ++j) {
+    const int raw = __ldg(slot_pos + t * k + j);
+    const int p = routed_row(raw, S, nullptr);
+    const int place = p >= 0 ? p : -1 - raw;   // the zero row of a dropped slot (skipped if it is out of range)
+    const float wj = p >= 0 ? __ldg(w + t * k + j) : 0.0f;
+    float dot = 0.0f;
+    for (int u = threadIdx.x; u < units; u += kThreads) {
+      float d[n], r[n];
+      Elems<V>::get(__ldg(dout + t * units + u), d);
+      if (p >= 0) {
+        float y[n];
+        Elems<V>::get(__ldg(ys + static_cast<int64_t>(p) * units + u), y);
+#pragma unroll
+        for (int c = 0; c < n; ++c) dot = fmaf(d[c], y[c], dot);
+      }
+#pragma unroll
+      for (int c = 0; c < n; ++c) r[c] = p >= 0 ? wj * d[c] : 0.0f;
+      if (place >= 0 && place < S) dys[static_cast<int64_t>(place) * units + u] = Elems<V>::put(r);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    if (lane == 0) s_dot[j][warp] = dot;
+  }
+  __syncthreads();
+  if (threadIdx.x < k) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) v += s_dot[threadIdx.x][i];
+    dw[t * k + threadIdx.x] = v;
+  }
+}
+
+int units_of(const SortShape& s) { return s.H * (s.fp32 ? 4 : 2) / 16; }
+
+}  // namespace
+
+int64_t sort_chunks(int64_t S) { return (S + kChunk - 1) / kChunk; }
+
+// Up to this many slots every CTA counts the ranks itself; above, the counting sort's four launches.
+constexpr int kRankMaxSlots = 2048;
+
+cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t* ids, void* xs, int32_t* offsets,
+                               int32_t* sorted_slot, int32_t* slot_pos, int32_t* hist, int32_t* totals, int32_t* status,
+                               cudaStream_t st) {
+  const int units = units_of(s);
+  const int S = s.T * s.k;
+  const uint4* xv = static_cast<const uint4*>(x);
+  uint4* xo = static_cast<uint4*>(xs);
+  if (S <= kRankMaxSlots)
+    return launch_pdl(true, sort_rank_kernel, dim3(s.T), dim3(kThreads), sizeof(int) * S, st, xv, ids, s.T, units, s.E, s.k,
+                      xo, offsets, sorted_slot, slot_pos, status);
+  const int chunks = static_cast<int>(sort_chunks(S));
+  const size_t smem = sizeof(int) * kWarps * (s.E + 1);
+  cudaError_t e = launch_pdl(true, sort_count_kernel, dim3(chunks), dim3(kThreads), 0, st, ids, S, s.E, hist, status);
+  if (e == cudaSuccess)
+    e = launch_pdl(true, sort_scan_kernel, dim3(s.E / 32 + 1), dim3(1024), 0, st, hist, chunks, s.E, totals);
+  if (e == cudaSuccess)
+    e = launch_pdl(true, sort_place_kernel, dim3(chunks), dim3(kThreads), smem, st, ids, S, s.E,
+                   static_cast<const int32_t*>(hist), static_cast<const int32_t*>(totals), offsets, sorted_slot, slot_pos);
+  if (e == cudaSuccess)
+    e = launch_pdl(true, sort_gather_kernel, dim3(s.T), dim3(std::min(kThreads, (units + 31) / 32 * 32)), 0, st, xv,
+                   static_cast<const int32_t*>(slot_pos), units, s.k, xo);
+  return e;
+}
+
+cudaError_t launch_return_tokens(const SortShape& s, const void* rows, const int32_t* slot_pos, const float* w,
+                                 const void* shared, void* out, cudaStream_t st) {
+  const int units = units_of(s);
+  const int64_t blocks = (static_cast<int64_t>(s.T) * units + kThreads - 1) / kThreads;
+  auto kern = s.fp32 ? return_kernel<float> : return_kernel<uint16_t>;
+  return launch_pdl(true, kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st,
+                    static_cast<const uint4*>(rows), slot_pos, w, static_cast<const uint4*>(shared),
+                    static_cast<int64_t>(s.T), units, s.k, static_cast<uint4*>(out));
+}
+
+cudaError_t launch_return_tokens_grad(const SortShape& s, const void* dout, const void* ys, const int32_t* slot_pos,
+                                      const float* w, void* dys, float* dw, cudaStream_t st) {
+  const int units = units_of(s);
+  auto kern = s.fp32 ? return_grad_kernel<float> : return_grad_kernel<uint16_t>;
+  return launch_pdl(true, kern, dim3(s.T), dim3(kThreads), 0, st, static_cast<const uint4*>(dout),
+                    static_cast<const uint4*>(ys), slot_pos, w, static_cast<int64_t>(s.T), units, s.k,
+                    static_cast<uint4*>(dys), dw);
+}
+
+}  // namespace moe
