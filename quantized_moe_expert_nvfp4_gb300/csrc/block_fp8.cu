@@ -26,47 +26,48 @@ __device__ __forceinline__ uint32_t codes2(float a, float b, float inv) {
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3));
 }
 
-// One warp per row: 16 lanes hold a block (eight bf16 each).  codes [rows, 128 KB], zero from K
-// on; scales [rows, KB rounded up to 4], zero from KB on (KB = blocks of a row).
+// One warp per row and 1024 columns: 8 lanes hold a block (16 bf16 each), so every lane has its four
+// 16-byte loads in flight at once.  codes [rows, 128 KB], zero from K on; scales [rows, KB rounded
+// up to 4], zero from KB on (KB = blocks of a row).
+constexpr int kRowSteps = 2, kRowBlocks = 4 * kRowSteps;
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restrict__ x, int64_t rows, int K, int KB,
-                                                            uint2* __restrict__ codes, float* __restrict__ scales) {
+                                                            int tasks, uint4* __restrict__ codes,
+                                                            float* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
-  const int64_t r = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   pdl_wait();
+  const int64_t r = i / tasks;
   if (r >= rows) return;
-  const int units = K / 8, pitch = (KB + 3) & ~3;
-  const uint4* src = x + r * units;
-  uint2* dst = codes + r * KB * 16;
-  for (int kb0 = 0; kb0 < pitch; kb0 += 32) {   // 32 scales are written together
-    float mine = 0.0f;
-#pragma unroll 4
-    for (int b = 0; b < 32; b += 2) {
-      const int kb = kb0 + b + (lane >> 4);
-      if (kb0 + b >= KB) break;
-      const int u = kb * 16 + (lane & 15);
-      const uint4 q = u < units ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-      float v[8], amax = 0.0f;
+  const int kb0 = static_cast<int>(i - r * tasks) * kRowBlocks;
+  const int units = K / 16, pitch = (KB + 3) & ~3;
+  uint4 q[kRowSteps][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(v[i]));
-#pragma unroll
-      for (int d = 8; d > 0; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-      float inv, scale;
-      block_rule(amax, inv, scale);
-      if (kb < KB)
-        dst[u] = make_uint2(codes2(v[0], v[1], inv) | (codes2(v[2], v[3], inv) << 16),
-                            codes2(v[4], v[5], inv) | (codes2(v[6], v[7], inv) << 16));
-      // lane b of the 32 keeps the scale of block kb0 + b, lane b + 1 that of the next
-      const float s0 = __shfl_sync(0xffffffffu, scale, 0), s1 = __shfl_sync(0xffffffffu, scale, 16);
-      if (lane == b) mine = s0;
-      if (lane == b + 1 && kb0 + b + 1 < KB) mine = s1;
+  for (int s = 0; s < kRowSteps; ++s) {
+    const int u = kb0 * 8 + s * 32 + lane;
+    q[s][0] = q[s][1] = make_uint4(0, 0, 0, 0);
+    if (u < units) {
+      q[s][0] = __ldg(x + (r * units + u) * 2);
+      q[s][1] = __ldg(x + (r * units + u) * 2 + 1);
     }
-    if (kb0 + lane < pitch) scales[r * pitch + kb0 + lane] = mine;
+  }
+#pragma unroll
+  for (int s = 0; s < kRowSteps; ++s) {
+    const uint32_t w[8] = {q[s][0].x, q[s][0].y, q[s][0].z, q[s][0].w, q[s][1].x, q[s][1].y, q[s][1].z, q[s][1].w};
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+    for (int c = 1; c < 8; ++c) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[c])));
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float inv, scale;
+    block_rule(max_nan(__low2float(m), __high2float(m)), inv, scale);
+    uint32_t o[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      o[c] = codes2(__uint_as_float(w[2 * c] << 16), __uint_as_float(w[2 * c] & 0xffff0000u), inv) |
+             (codes2(__uint_as_float(w[2 * c + 1] << 16), __uint_as_float(w[2 * c + 1] & 0xffff0000u), inv) << 16);
+    const int kb = kb0 + s * 4 + (lane >> 3);
+    if (kb < KB) codes[r * KB * 8 + kb * 8 + (lane & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
+    if ((lane & 7) == 0 && kb < pitch) scales[r * pitch + kb] = kb < KB ? scale : 0.0f;
   }
 }
 
@@ -150,9 +151,10 @@ __global__ void __launch_bounds__(256) transpose_blocks_kernel(const uint32_t* _
 
 cudaError_t launch_quantize_rows_block(const uint16_t* x, int64_t rows, int K, uint8_t* codes, float* scales,
                                        cudaStream_t st) {
-  const int64_t blocks = (rows * 32 + 255) / 256;
+  const int KB = (K + 127) / 128, tasks = (KB + kRowBlocks - 1) / kRowBlocks;
+  const int64_t blocks = (rows * tasks + 7) / 8;
   return launch_pdl(true, quantize_rows_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
-                    reinterpret_cast<const uint4*>(x), rows, K, (K + 127) / 128, reinterpret_cast<uint2*>(codes), scales);
+                    reinterpret_cast<const uint4*>(x), rows, K, KB, tasks, reinterpret_cast<uint4*>(codes), scales);
 }
 
 cudaError_t launch_quantize_blocks(const void* w, bool fp32, int G, int N, int K, uint8_t* codes, float* scales,
