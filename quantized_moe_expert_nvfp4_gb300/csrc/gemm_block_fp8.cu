@@ -29,24 +29,33 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
+constexpr int kPromoteWgs = 2;                // promoting warpgroups
+constexpr int kThreads = 128 + 128 * kPromoteWgs;
 constexpr int kWarpTmaB = 0, kWarpMma = 1, kWarpTmaA = 2, kWarpAlloc = 3, kWarpPromote = 4;
+constexpr int kMaxStages = 6;
 constexpr int kChunk = 128;                    // K of a scale block: one 128-byte swizzled row
-constexpr int kBStage = 32768;
 constexpr uint32_t kSpinLimit = 1u << 24;      // drain loops only
 constexpr uint64_t kWaitTimeoutNs = 1000000000ull;
 
-// BN: columns of a tile (MMA N); kRows: rows of a tile at most.
-template <int BN, int kRows>
+// BN: columns of a tile (MMA N); kRows: rows of a tile that a CTA holds at most.  kPair: a cluster of
+// two CTAs takes a tile of 2 kRows rows with one cta_group::2 MMA; each holds its own rows, half of
+// the matrix tile, and the accumulator of its rows.
+template <int BN, int kRows, bool kPair>
 struct Tile {
-  static constexpr int kChunks = 256 / BN;                     // K chunks per stage
+  static constexpr int kTileRows = kPair ? 2 * kRows : kRows;
+  static constexpr int kBRows = kPair ? BN / 2 : BN;           // matrix rows in this CTA's shared memory
+  static constexpr int kChunks = kPair ? 1 : 256 / BN;         // K chunks per stage
   static constexpr int kAStage = kChunks * kRows * kChunk;
-  static constexpr int kStages = std::min(4, 196608 / (kAStage + kBStage));
+  static constexpr int kBStage = kChunks * kBRows * kChunk;
   static constexpr int kBufs = std::min(4, 512 / BN);          // TMEM accumulators
   static constexpr int kTmemCols = kBufs * BN;
-  static constexpr int kCols = BN / 2;                         // columns per promoting thread
+  static constexpr int kCols = BN / kPromoteWgs;               // columns per promoting thread
   static constexpr int kBoxes = kRows / 16;
-  static constexpr int kActive = kRows / 32 * 2;               // promotion warps with rows
+  static constexpr int kWarps = kRows / 32 * kPromoteWgs;      // promoting warps with rows
+  static constexpr int kBoxesOut = kCols / 64;                 // staged boxes of 32 rows x 128 bytes per warp
+  static constexpr int kStaging = kWarps * kBoxesOut * 4096;
+  static constexpr int kStages = std::min(kMaxStages, (220160 - kStaging) / (kAStage + kBStage));
+  static constexpr int kSmem = 1024 + kStages * (kAStage + kBStage) + kStaging;
 };
 
 template <int kBoxes>
@@ -55,30 +64,93 @@ struct Maps {
   CUtensorMap b;                 // matrix codes, kChunks chunks
   CUtensorMap b_one;             // one chunk
   CUtensorMap b_tail;            // the last chunk of a K that is no multiple of 128
+  CUtensorMap out;               // bf16 output, a box of 32 rows x 64 columns
 };
 
 struct Bars {
-  uint64_t full[4], empty[4];           // stage: two arrivals (matrix and rows), one commit
+  uint64_t full[kMaxStages], empty[kMaxStages];   // stage: two arrivals (matrix and rows), one commit
   uint64_t acc_full[4], acc_empty[4];
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
 };
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* tm, int x, int y, int z, int w, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
+// Loads of a CTA pair may signal the barrier of either CTA (bar: a shared::cluster address).
+template <bool kPair>
+__device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+template <bool kPair>
+__device__ __forceinline__ void load_4d(void* dst, const CUtensorMap* tm, int x, int y, int z, int w, uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
 }
 
+template <bool kPair>
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrival, on this barrier of the CTAs in `ctas`, when the MMAs issued so far have completed.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* b, int ctas = 3) {
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(b)),
+        "h"(static_cast<uint16_t>(ctas))
+        : "memory");
+  else
+    tc_commit(b);
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Relaxed: the arrival orders TMEM reads only, which the tcgen05 fence before it covers (a release at
+// cluster scope took longer than the block's MMAs).
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
@@ -99,104 +171,154 @@ __device__ __forceinline__ uint32_t bf16x2(uint64_t v) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 32 bytes of one row (32-byte aligned)
-__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 
-// Stores a thread's kCols columns from column n on of its row.  32-byte stores where rows start on
-// 32 bytes (measured against two 16-byte stores: the latter send half sectors), else per element.
+// Stores a thread's kCols columns from column n on of its row, element by element (rows that do not
+// start on 16 bytes).
 template <int kCols>
-__device__ __forceinline__ void store_row(const BlockFp8Args& a, int64_t row, int n, const uint64_t (&acc)[kCols / 2],
-                                          bool vec) {
-  if (a.out_fp32) {
-    float* dst = static_cast<float*>(a.out) + row * a.N + n;
-    if (vec) {
+__device__ __forceinline__ void store_row(const BlockFp8Args& a, int64_t row, int n, const uint64_t (&acc)[kCols / 2]) {
 #pragma unroll
-      for (int c = 0; c < kCols; c += 8) {
-        if (n + c < a.N) {
-          uint32_t w[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2(acc[c / 2 + i]);
-            w[2 * i] = __float_as_uint(f.x);
-            w[2 * i + 1] = __float_as_uint(f.y);
-          }
-          store32(dst + c, w);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < kCols; c += 2) {
-        const float2 f = unpack2(acc[c / 2]);
-        if (n + c < a.N) dst[c] = f.x;
-        if (n + c + 1 < a.N) dst[c + 1] = f.y;
-      }
-    }
-  } else {
-    uint16_t* dst = static_cast<uint16_t*>(a.out) + row * a.N + n;
-    if (vec) {
-#pragma unroll
-      for (int c = 0; c < kCols; c += 16) {
-        if (n + c < a.N) {
-          uint32_t w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = bf16x2(acc[c / 2 + i]);
-          store32(dst + c, w);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < kCols; c += 2) {
-        const uint32_t h = bf16x2(acc[c / 2]);
-        if (n + c < a.N) dst[c] = static_cast<uint16_t>(h);
-        if (n + c + 1 < a.N) dst[c + 1] = static_cast<uint16_t>(h >> 16);
-      }
-    }
+  for (int c = 0; c < kCols; ++c) {
+    const float2 f = unpack2(acc[c / 2]);
+    const float v = c & 1 ? f.y : f.x;
+    if (n + c >= a.N) continue;
+    if (a.out_fp32) static_cast<float*>(a.out)[row * a.N + n + c] = v;
+    else static_cast<uint16_t*>(a.out)[row * a.N + n + c] = f32_to_bf16_bits(v);
   }
 }
 
-template <int BN, int kRows>
+// Stores a warp's rows (one per lane) through shared memory, 128 bytes of each row in a box of 4 KB
+// (the 128-byte swizzle of the output's tensor map).  Written straight from the registers, each of
+// a store instruction's 32 rows is a line of its own, and the stores of a 256 x 256 tile held the
+// promoting warps for 1.7 us.  32 full rows of bf16 leave as bulk copies that nothing waits for but
+// the next tile's staging; other rows as lines of a few rows per store.
+template <int kCols>
+__device__ __forceinline__ void store_staged(const BlockFp8Args& a, const CUtensorMap* out_map, uint8_t* stage, int lane,
+                                             int row0, int rows, int n, const uint64_t (&acc)[kCols / 2]) {
+  const int row_bytes = a.N * (a.out_fp32 ? 4 : 2);
+  auto unit_at = [&](int box, int r, int u) { return stage + box * 4096 + r * 128 + ((u ^ (r & 7)) << 4); };
+  auto flush = [&](int box, int byte0) {   // a staged box, to the columns from byte0 of the rows on
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * 4 + lane / 8, u = lane % 8, at = byte0 + u * 16;
+      if (r < rows && at < row_bytes)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + static_cast<int64_t>(row0 + r) * row_bytes + at) =
+            *reinterpret_cast<const uint4*>(unit_at(box, r, u));
+    }
+  };
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // the last tile's copies have read the boxes
+  __syncwarp();
+  if (a.out_fp32) {
+    for (int half = 0; half < 2; ++half) {   // the boxes hold half of the columns at a time
+#pragma unroll
+      for (int box = 0; box < kCols / 64; ++box) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int c = (box * 32 + 4 * u) / 2;   // of the first half
+          const float2 p = unpack2(half ? acc[kCols / 4 + c] : acc[c]), q = unpack2(half ? acc[kCols / 4 + c + 1] : acc[c + 1]);
+          *reinterpret_cast<float4*>(unit_at(box, lane, u)) = make_float4(p.x, p.y, q.x, q.y);
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int box = 0; box < kCols / 64; ++box) flush(box, (n + half * (kCols / 2) + box * 32) * 4);
+      __syncwarp();
+    }
+    return;
+  }
+#pragma unroll
+  for (int box = 0; box < kCols / 64; ++box)
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int c = (box * 64 + 8 * u) / 2;
+      *reinterpret_cast<uint4*>(unit_at(box, lane, u)) =
+          make_uint4(bf16x2(acc[c]), bf16x2(acc[c + 1]), bf16x2(acc[c + 2]), bf16x2(acc[c + 3]));
+    }
+  if (rows == 32) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+#pragma unroll
+      for (int box = 0; box < kCols / 64; ++box)
+        if (n + box * 64 < a.N)
+          asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(out_map),
+                       "r"(n + box * 64), "r"(row0), "r"(smem_u32(stage + box * 4096))
+                       : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  } else {
+    __syncwarp();
+#pragma unroll
+    for (int box = 0; box < kCols / 64; ++box) flush(box, (n + box * 64) * 2);
+  }
+}
+
+// The items (row tile, column tile) of one CTA or pair: item i, i + n, i + 2 n, ... of n, column
+// tiles of a row tile first.
+struct Items {
+  int tile, nt, step_tile, step_nt, NT, tiles;
+  __device__ __forceinline__ Items(int i, int n, int nt_count, int tile_count)
+      : tile(i / nt_count), nt(i % nt_count), step_tile(n / nt_count), step_nt(n % nt_count), NT(nt_count), tiles(tile_count) {}
+  __device__ __forceinline__ bool more() const { return tile < tiles; }
+  __device__ __forceinline__ void next() {
+    tile += step_tile;
+    nt += step_nt;
+    if (nt >= NT) {
+      nt -= NT;
+      ++tile;
+    }
+  }
+};
+
+template <int BN, int kRows, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
-    block_fp8_kernel(const __grid_constant__ Maps<Tile<BN, kRows>::kBoxes> maps, BlockFp8Args a, bool vec) {
-  using C = Tile<BN, kRows>;
+    block_fp8_kernel(const __grid_constant__ Maps<Tile<BN, kRows, kPair>::kBoxes> maps, BlockFp8Args a, bool vec) {
+  using C = Tile<BN, kRows, kPair>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ GroupTiles gt;
   __shared__ Bars sm;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = base;                                // row tiles first: reads past a short tile stay inside
   uint8_t* sB = base + C::kStages * C::kAStage;
+  uint8_t* sOut = sB + C::kStages * C::kBStage;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = kPair ? cluster_rank() : 0;    // rank 0 of a pair issues the MMAs
   const int NT = (a.N + BN - 1) / BN;
   const int KB = (a.K + kChunk - 1) / kChunk, KF = a.K / kChunk;
   const int KS = (KB + C::kChunks - 1) / C::kChunks;   // stages per item
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sm.full[s], 2);
       mbar_init(&sm.empty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
       mbar_init(&sm.acc_full[s], 1);
-      mbar_init(&sm.acc_empty[s], C::kActive);
+      mbar_init(&sm.acc_empty[s], C::kWarps * (kPair ? 2 : 1));
     }
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWarpAlloc) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
-                 "r"(C::kTmemCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                   "r"(C::kTmemCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
+                   "r"(C::kTmemCols));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
   }
   pdl_wait();
-  build_group_tiles(gt, a.offsets, a.G, a.M, kRows, a.status);
+  build_group_tiles(gt, a.offsets, a.G, a.M, C::kTileRows, a.status);
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_barrier();              // both CTAs' barriers are initialised
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  const int64_t items = static_cast<int64_t>(gt.first[a.G + 1]) * NT;
+  Items it(kPair ? blockIdx.x / 2 : blockIdx.x, kPair ? gridDim.x / 2 : gridDim.x, NT, gt.first[a.G + 1]);
   auto wait = [&](uint64_t* b, uint32_t parity) {
     return mbar_wait_flag(b, parity, &sm.abort_flag, a.status, kWaitTimeoutNs);
   };
@@ -206,52 +328,64 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < kWarpPromote) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // 384 threads launch with 168 registers each: 128 x 72 + 256 x 216, or 128 x 88 + 256 x 208
+    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpTmaB || warp == kWarpTmaA) {
       if (lane == 0) {
         uint32_t is = 0;
         bool ok = true;
-        for (int64_t item = blockIdx.x; ok && item < items; item += gridDim.x) {
-          const RowTile rt = group_tile(gt, a.G, static_cast<int>(item / NT), kRows);
+        for (; ok && it.more(); it.next()) {
+          const RowTile rt = group_tile(gt, a.G, it.tile, C::kTileRows);
           if (rt.group == a.G) continue;
-          const int n0 = static_cast<int>(item % NT) * BN;
-          const int n16 = (rt.rows + 15) >> 4;
+          const int n0 = it.nt * BN + static_cast<int>(rank) * C::kBRows;
+          // rows of each CTA, in boxes of 16, one at least: a producer without a load in a stage
+          // would not hold the ring back and could be overtaken.  The leader's barrier counts both
+          // CTAs' bytes.
+          const int box0 = (min(rt.rows, kRows) + 15) >> 4, box1 = (max(rt.rows - kRows, 1) + 15) >> 4;
+          const int box = rank == 0 ? box0 : box1;
           for (int s = 0; s < KS; ++s, ++is) {
             const int st = is % C::kStages, kb0 = s * C::kChunks;
             if (!(ok = wait(&sm.empty[st], ((is / C::kStages) & 1) ^ 1))) break;
+            const uint32_t bar = kPair ? cluster_addr(&sm.full[st], 0) : smem_u32(&sm.full[st]);
             if (warp == kWarpTmaA) {
-              mbar_expect_tx(&sm.full[st], C::kChunks * n16 * 16 * kChunk);
-              tma_load_3d(sA + st * C::kAStage, &maps.a[n16 - 1], 0, rt.row, kb0, &sm.full[st]);
+              if (rank == 0) mbar_expect_tx(&sm.full[st], C::kChunks * (box0 + (kPair ? box1 : 0)) * 16 * kChunk);
+              load_3d<kPair>(sA + st * C::kAStage, &maps.a[box - 1], 0, rt.row + static_cast<int>(rank) * kRows, kb0, bar);
             } else if (kb0 + C::kChunks <= KF) {
-              mbar_expect_tx(&sm.full[st], kBStage);
-              tma_load_4d(sB + st * kBStage, &maps.b, 0, n0, kb0, rt.group, &sm.full[st]);
+              if (rank == 0) mbar_expect_tx(&sm.full[st], C::kBStage * (kPair ? 2 : 1));
+              load_4d<kPair>(sB + st * C::kBStage, &maps.b, 0, n0, kb0, rt.group, bar);
             } else {   // the last stage, chunk by chunk
-              mbar_expect_tx(&sm.full[st], (KB - kb0) * BN * kChunk);
+              if (rank == 0) mbar_expect_tx(&sm.full[st], (KB - kb0) * C::kBRows * kChunk * (kPair ? 2 : 1));
               for (int kb = kb0; kb < KB; ++kb) {
-                uint8_t* dst = sB + st * kBStage + (kb - kb0) * BN * kChunk;
-                if (kb < KF) tma_load_4d(dst, &maps.b_one, 0, n0, kb, rt.group, &sm.full[st]);
-                else tma_load_3d(dst, &maps.b_tail, kb * kChunk, n0, rt.group, &sm.full[st]);
+                uint8_t* dst = sB + st * C::kBStage + (kb - kb0) * C::kBRows * kChunk;
+                if (kb < KF) load_4d<kPair>(dst, &maps.b_one, 0, n0, kb, rt.group, bar);
+                else load_3d<kPair>(dst, &maps.b_tail, kb * kChunk, n0, rt.group, bar);
               }
             }
           }
         }
+        if (kPair && ok) {   // the MMAs' last arrivals reach this CTA before it ends
+          const uint32_t last = is;
+          for (uint32_t j = last > C::kStages ? last - C::kStages : 0; ok && j < last; ++j)
+            ok = wait(&sm.empty[j % C::kStages], (j / C::kStages) & 1);
+        }
         if (!ok) {   // let copies already issued land before the CTA winds down (bounded)
           for (int j = 0; j < C::kStages && is > 0; ++j, --is) {
             const uint32_t q = is - 1;
-            for (uint32_t i = 0; i < (1u << 16) && !mbar_try(&sm.full[q % C::kStages], (q / C::kStages) & 1); ++i) {
+            uint64_t* b = rank == 0 ? &sm.full[q % C::kStages] : &sm.empty[q % C::kStages];
+            for (uint32_t i = 0; i < (1u << 16) && !mbar_try(b, (q / C::kStages) & 1); ++i) {
             }
           }
         }
       }
-    } else if (warp == kWarpMma) {
-      constexpr uint32_t idesc_rows = 128;
-      const uint32_t idesc = idesc_f32acc(idesc_rows, BN);
+    } else if (warp == kWarpMma && rank == 0) {
+      const uint32_t idesc = idesc_f32acc(kPair ? 256 : 128, BN);
       uint32_t is = 0, ib = 0;
       bool ok = true;
-      for (int64_t item = blockIdx.x; ok && item < items; item += gridDim.x) {
-        const RowTile rt = group_tile(gt, a.G, static_cast<int>(item / NT), kRows);
+      for (; ok && it.more(); it.next()) {
+        const RowTile rt = group_tile(gt, a.G, it.tile, C::kTileRows);
         if (rt.group == a.G) continue;
-        const int a_chunk = ((rt.rows + 15) & ~15) * kChunk;
+        const int a_chunk = ((min(rt.rows, kRows) + 15) & ~15) * kChunk;
         for (int s = 0; ok && s < KS; ++s, ++is) {
           const int st = is % C::kStages;
           if (!(ok = warp_wait(&sm.full[st], (is / C::kStages) & 1))) break;
@@ -262,105 +396,131 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (elect_one()) {
               const uint32_t aa = smem_u32(sA + st * C::kAStage) + c * a_chunk;
-              const uint32_t ba = smem_u32(sB + st * kBStage) + c * BN * kChunk;
+              const uint32_t ba = smem_u32(sB + st * C::kBStage) + c * C::kBRows * kChunk;
 #pragma unroll
               for (int kk = 0; kk < kChunk / 32; ++kk)
-                mma_e4m3(tmem + buf * BN, smem_desc_sw128(aa + kk * 32), smem_desc_sw128(ba + kk * 32), idesc, kk != 0);
-              tc_commit(&sm.acc_full[buf]);
+                mma_e4m3<kPair>(tmem + buf * BN, smem_desc_sw128(aa + kk * 32), smem_desc_sw128(ba + kk * 32), idesc, kk != 0);
+              commit<kPair>(&sm.acc_full[buf]);
             }
             __syncwarp();
           }
           if (!ok) break;
-          if (elect_one()) tc_commit(&sm.empty[st]);
+          if (elect_one()) commit<kPair>(&sm.empty[st]);
           __syncwarp();
         }
       }
       if (elect_one()) {   // every MMA issued completes before TMEM is released (bounded)
-        tc_commit(&sm.drain);
+        commit<kPair>(&sm.drain, 1);
         for (uint32_t i = 0; i < kSpinLimit && !mbar_try(&sm.drain, 0); ++i) {
         }
       }
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int q = warp & 3, half = (warp - kWarpPromote) >> 2;
+    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int q = warp & 3, wg = (warp - kWarpPromote) >> 2;
     if (q * 32 < kRows) {
-      const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * C::kCols;
+      const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + wg * C::kCols;
       const int NB = (a.N + 127) / 128, pitch = (KB + 3) & ~3;
       uint32_t ib = 0;
       bool ok = true;
-      for (int64_t item = blockIdx.x; ok && item < items; item += gridDim.x) {
-        const RowTile rt = group_tile(gt, a.G, static_cast<int>(item / NT), kRows);
-        const int n0 = static_cast<int>(item % NT) * BN + half * C::kCols;
-        const bool mine = q * 32 + lane < rt.rows;
-        const int64_t row = rt.row + (mine ? q * 32 + lane : 0);
+      const int r0 = static_cast<int>(rank) * kRows + q * 32;   // this warp's first row of the tile
+      uint8_t* stage = sOut + (wg * (kRows / 32) + q) * C::kBoxesOut * 4096;
+      // an item and its first scales, read before the previous item is stored
+      struct Job {
+        int group, row0, rows, n0;             // this warp's rows (none or fewer than 32 at a group's end)
+        const float *sx, *sw;
+        float x, w;
+      };
+      auto job_of = [&](const Items& i) {
+        const RowTile rt = group_tile(gt, a.G, i.tile, C::kTileRows);
+        Job j;
+        j.group = rt.group;
+        j.row0 = rt.row + r0;
+        j.rows = min(32, rt.rows - r0);
+        j.n0 = i.nt * BN + wg * C::kCols;
+        if (rt.group < a.G) {
+          j.sx = a.x_scales + static_cast<int64_t>(lane < j.rows ? j.row0 + lane : rt.row) * pitch;
+          j.sw = a.w_scales + (static_cast<int64_t>(rt.group) * NB + min(j.n0 / 128, NB - 1)) * KB;
+          j.x = __ldg(j.sx);
+          j.w = __ldg(j.sw);
+        }
+        return j;
+      };
+      Job job;
+      if (it.more()) job = job_of(it);
+      while (ok && it.more()) {
         uint64_t acc[C::kCols / 2];
 #pragma unroll
         for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
-        if (rt.group < a.G) {
-          const bool some = q * 32 < rt.rows;             // rows of this warp
-          const float4* sx = reinterpret_cast<const float4*>(a.x_scales + row * pitch);
-          const float* sw = a.w_scales + (static_cast<int64_t>(rt.group) * NB + min(n0 / 128, NB - 1)) * KB;
-          // scales of four blocks at a time, the next four in flight
-          float4 x_next = __ldg(sx);
-          float w_next[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w_next[i] = i < KB ? __ldg(sw + i) : 0.0f;
-          for (int kb0 = 0; ok && kb0 < KB; kb0 += 4) {
-            const float sc[4] = {x_next.x * w_next[0], x_next.y * w_next[1], x_next.z * w_next[2], x_next.w * w_next[3]};
-            if (kb0 + 4 < KB) {
-              x_next = __ldg(sx + kb0 / 4 + 1);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w_next[i] = kb0 + 4 + i < KB ? __ldg(sw + kb0 + 4 + i) : 0.0f;
+        if (job.group < a.G) {
+          for (int kb = 0; kb < KB; ++kb, ++ib) {
+            const uint32_t sc = __float_as_uint(job.x * job.w);
+            const uint64_t s2 = pack2(sc, sc);
+            if (kb + 1 < KB) {               // the next block's, in flight during this block
+              job.x = __ldg(job.sx + kb + 1);
+              job.w = __ldg(job.sw + kb + 1);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (kb0 + i >= KB) break;
-              const int buf = ib % C::kBufs;
-              if (!(ok = warp_wait(&sm.acc_full[buf], (ib / C::kBufs) & 1))) break;
-              ++ib;
-              tc_fence_after();
-              if (some) {
-                const uint64_t s2 = pack2(__float_as_uint(sc[i]), __float_as_uint(sc[i]));
-                const uint32_t t = t_lane + buf * BN;
-                uint32_t v[2][16];
-                TC_LD16(t, v[0]);
-#pragma unroll
-                for (int c = 0; c < C::kCols; c += 16) {
-                  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                  if (c + 16 < C::kCols) TC_LD16(t + c + 16, v[(c / 16 + 1) & 1]);
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) fma2(acc[c / 2 + j], pack2(v[(c / 16) & 1][2 * j], v[(c / 16) & 1][2 * j + 1]), s2);
-                }
-              }
+            const int buf = ib % C::kBufs;
+            if (!(ok = warp_wait(&sm.acc_full[buf], (ib / C::kBufs) & 1))) break;
+            tc_fence_after();
+            auto release = [&] {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&sm.acc_empty[buf]);
+              if (lane == 0) {
+                if constexpr (kPair) arrive_at(cluster_addr(&sm.acc_empty[buf], 0));
+                else mbar_arrive(&sm.acc_empty[buf]);
+              }
+            };
+            if (job.rows > 0) {
+              const uint32_t t = t_lane + buf * BN;
+#pragma unroll
+              for (int c = 0; c < C::kCols; c += 32) {
+                uint32_t v[2][16];
+                TC_LD16(t + c, v[0]);
+                TC_LD16(t + c + 16, v[1]);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                if (c + 32 >= C::kCols) release();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) fma2(acc[c / 2 + j], pack2(v[j / 8][2 * (j % 8)], v[j / 8][2 * (j % 8) + 1]), s2);
+              }
+            } else {
+              release();
             }
           }
         }
-        if (ok && mine && n0 < a.N) store_row<C::kCols>(a, row, n0, acc, vec);
+        const Job done = job;
+        it.next();
+        if (ok && it.more()) job = job_of(it);
+        if (ok && done.n0 < a.N && done.rows > 0) {
+          if (vec) store_staged<C::kCols>(a, &maps.out, stage, lane, done.row0, done.rows, done.n0, acc);
+          else if (lane < done.rows) store_row<C::kCols>(a, done.row0 + lane, done.n0, acc);
+        }
         __syncwarp();
       }
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (kPair) cluster_barrier();   // neither CTA's shared memory or TMEM is used any more
   if (warp == kWarpAlloc) {
     __syncwarp();
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
+    if constexpr (kPair)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
   }
 }
 
-template <int BN, int kRows>
+template <int BN, int kRows, bool kPair>
 cudaError_t launch_tile(const BlockFp8Args& a, int n_sm, cudaStream_t st) {
-  using C = Tile<BN, kRows>;
-  constexpr int smem = 1024 + C::kStages * (C::kAStage + kBStage);
-  auto kern = block_fp8_kernel<BN, kRows>;
-  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem);
+  using C = Tile<BN, kRows, kPair>;
+  auto kern = block_fp8_kernel<BN, kRows, kPair>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), C::kSmem);
   if (e != cudaSuccess) return e;
   const uint64_t M = a.M, N = a.N, K = a.K, G = a.G, KB = (K + kChunk - 1) / kChunk, KF = K / kChunk;
   Maps<C::kBoxes> maps;
@@ -372,21 +532,41 @@ cudaError_t launch_tile(const BlockFp8Args& a, int n_sm, cudaStream_t st) {
   }
   if (ok && KF > 0) {
     const uint64_t dims[4] = {kChunk, N, KF, G}, strides[3] = {K, kChunk, N * K};
-    const uint32_t box[4] = {kChunk, BN, C::kChunks, 1}, one[4] = {kChunk, BN, 1, 1};
+    const uint32_t box[4] = {kChunk, C::kBRows, C::kChunks, 1}, one[4] = {kChunk, C::kBRows, 1, 1};
     ok = make_tensor_map(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.w_codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
          make_tensor_map(&maps.b_one, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.w_codes, dims, strides, one, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (ok && K % kChunk) {
     const uint64_t dims[3] = {K, N, G}, strides[2] = {K, N * K};
-    const uint32_t box[3] = {kChunk, BN, 1};
+    const uint32_t box[3] = {kChunk, C::kBRows, 1};
     ok = make_tensor_map(&maps.b_tail, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.w_codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const bool vec = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && N % (a.out_fp32 ? 8 : 16) == 0;
+  const bool vec = N % (a.out_fp32 ? 4 : 8) == 0;   // rows start on 16 bytes
+  if (vec && !a.out_fp32) {
+    const uint64_t dims[2] = {N, M}, strides[1] = {2 * N};
+    const uint32_t box[2] = {64, 32};
+    if (!make_tensor_map(&maps.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
   // tiles at most: one per full tile of rows and one more per group that has rows
-  const int64_t most = (M / kRows + std::min(M, G + 1)) * ((N + BN - 1) / BN);
-  const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, n_sm)));
-  return launch_pdl(true, kern, dim3(grid), dim3(kThreads), smem, st, maps, a, vec);
+  const int64_t most = (M / C::kTileRows + std::min(M, G + 1)) * ((N + BN - 1) / BN);
+  const int64_t ctas = kPair ? std::min<int64_t>(2 * most, n_sm / 2 * 2) : std::min<int64_t>(most, n_sm);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(kPair ? 2 : 1, ctas)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, a, vec);
 }
 
 }  // namespace
@@ -396,8 +576,9 @@ cudaError_t launch_block_fp8_matmul(const BlockFp8Args& a, cudaStream_t st) {
   cudaError_t e = current_sm_count(&n_sm);
   if (e != cudaSuccess) return e;
   const int64_t large = (a.M / 128 + std::min<int64_t>(a.M, a.G)) * ((a.N + 255) / 256);
-  if (a.M <= 16 * static_cast<int64_t>(a.G) || large < n_sm) return launch_tile<64, 32>(a, n_sm, st);
-  return launch_tile<256, 128>(a, n_sm, st);
+  if (a.M <= 16 * static_cast<int64_t>(a.G) || large < n_sm) return launch_tile<128, 32, false>(a, n_sm, st);
+  if (a.M >= 256 * static_cast<int64_t>(a.G)) return launch_tile<256, 128, true>(a, n_sm, st);
+  return launch_tile<256, 128, false>(a, n_sm, st);
 }
 
 }  // namespace moe
