@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
                                                             float* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  pdl_wait();
+  pdl_wait_then_release();   // the product's launch starts with this grid's last wave
   const int64_t r = i / tasks;
   if (r >= rows) return;
   const int kb0 = static_cast<int>(i - r * tasks) * kRowBlocks;

@@ -311,7 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
   }
-  pdl_wait();
+  // Matrices and offsets are read before the wait for the previous launch, the row quantizer: it
+  // lets this kernel start only after its own wait, that is, after everything before it.  Only the
+  // row codes and scales (the row producer, the promotion) depend on the quantizer itself.
   build_group_tiles(gt, a.offsets, a.G, a.M, C::kTileRows, a.status);
   tc_fence_before();
   __syncthreads();
@@ -328,13 +330,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < kWarpPromote) {
-    // 384 threads launch with 168 registers each: 128 x 72 + 256 x 216, or 128 x 88 + 256 x 208
-    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // 384 threads launch with 168 registers each: 128 x 40 + 256 x 232 of the same total
+    // (or 88 and 208 of the smaller tile)
+    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpTmaB || warp == kWarpTmaA) {
       if (lane == 0) {
         uint32_t is = 0;
         bool ok = true;
+        if (warp == kWarpTmaA) pdl_wait();
         for (; ok && it.more(); it.next()) {
           const RowTile rt = group_tile(gt, a.G, it.tile, C::kTileRows);
           if (rt.group == a.G) continue;
@@ -383,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t is = 0, ib = 0;
       bool ok = true;
       for (; ok && it.more(); it.next()) {
-        const RowTile rt = group_tile(gt, a.G, it.tile, C::kTileRows);
+        const RowTile rt = group_tile_warp(gt, a.G, it.tile, C::kTileRows, lane);
         if (rt.group == a.G) continue;
         const int a_chunk = ((min(rt.rows, kRows) + 15) & ~15) * kChunk;
         for (int s = 0; ok && s < KS; ++s, ++is) {
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else {
-    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int q = warp & 3, wg = (warp - kWarpPromote) >> 2;
     if (q * 32 < kRows) {
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float x, w;
       };
       auto job_of = [&](const Items& i) {
-        const RowTile rt = group_tile(gt, a.G, i.tile, C::kTileRows);
+        const RowTile rt = group_tile_warp(gt, a.G, i.tile, C::kTileRows, lane);
         Job j;
         j.group = rt.group;
         j.row0 = rt.row + r0;
@@ -448,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return j;
       };
+      pdl_wait();
       Job job;
       if (it.more()) job = job_of(it);
       while (ok && it.more()) {

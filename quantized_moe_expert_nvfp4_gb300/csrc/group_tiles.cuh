@@ -79,4 +79,19 @@ __device__ __forceinline__ RowTile group_tile(const GroupTiles& g, int G, int ti
   return r;
 }
 
+// The same by a whole warp in two probes: 33 keys apart, then the 33 in between (a probe of shared
+// memory takes 100 cycles and more while the tensor cores read their operands from it).
+__device__ __forceinline__ RowTile group_tile_warp(const GroupTiles& g, int G, int tile, int tile_rows, int lane) {
+  static_assert(kMaxGroups + 1 <= 33 * 32, "two probes of 32");
+  int at = lane * 33;
+  unsigned below = __ballot_sync(0xffffffffu, at <= G && g.first[min(at, G)] <= tile);
+  at = (__popc(below) - 1) * 33 + 1 + lane;
+  below = __ballot_sync(0xffffffffu, at <= G && g.first[min(at, G)] <= tile);
+  RowTile r;
+  r.group = at - 1 - lane + __popc(below);
+  r.row = g.off[r.group] + (tile - g.first[r.group]) * tile_rows;
+  r.rows = min(tile_rows, g.off[r.group + 1] - r.row);
+  return r;
+}
+
 }  // namespace moe
