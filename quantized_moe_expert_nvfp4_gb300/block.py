@@ -12,7 +12,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import MoeError, _check, _ptr, _stream, load
+from . import MoeError, _check, _stream, load
+from . import _ptr as _checked_ptr
 
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_ELEMENT = 0, 1, 2, 3
 
@@ -58,23 +59,38 @@ def declare(L):
         fn.argtypes, fn.restype = args, res
 
 
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _ptr(t: torch.Tensor | None, dtype=None, name="tensor"):
+    """The address of a contiguous CUDA tensor of the type, as the package's _ptr checks it (a plain int:
+    a decode step's calls take as long as their Python)."""
+    if t is None:
+        return None
+    if (dtype is None or t.dtype is dtype) and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _checked_ptr(t, dtype, name)
+
+
 def _row_type(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
+    dtype = t.dtype
+    if dtype is _BF16:
         return 0
-    if t.dtype == torch.float32:
+    if dtype is _F32:
         return 1
     raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
 
 
 def _shaped(t: torch.Tensor | None, shape: tuple, name: str) -> None:
-    if t is not None and tuple(t.shape) != shape:
+    if t is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
 def _out(t: torch.Tensor | None, shape: tuple, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
     if t is None:
         return torch.empty(shape, dtype=dtype, device=like.device)
-    _shaped(t, shape, name)
+    if t.shape != shape:
+        _shaped(t, shape, name)
     return t
 
 
@@ -100,7 +116,7 @@ def sort_tokens(x, topk_ids, E: int, ws, xs=None, offsets=None, sorted_slot=None
     _shaped(topk_ids, (T, k), "topk_ids")
     S = T * k
     fp32 = _row_type(x, "x")
-    i32 = torch.int32
+    i32 = _I32
     xs = _out(xs, (S, H), x.dtype, x, "xs")
     offsets = _out(offsets, (E + 1,), i32, x, "offsets")
     sorted_slot = _out(sorted_slot, (S,), i32, x, "sorted_slot")
@@ -108,7 +124,7 @@ def sort_tokens(x, topk_ids, E: int, ws, xs=None, offsets=None, sorted_slot=None
     _check("moe_sort_tokens", load().moe_sort_tokens(
         _ptr(x), _ptr(topk_ids, i32, "topk_ids"), MoeTokens(T, H, E, k, fp32), _ptr(xs, x.dtype, "xs"),
         _ptr(offsets, i32, "offsets"), _ptr(sorted_slot, i32, "sorted_slot"), _ptr(slot_pos, i32, "slot_pos"),
-        _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+        _ptr(ws, _U8, "ws"), ws.numel(), _stream(stream)))
     return xs, offsets, sorted_slot, slot_pos
 
 
@@ -124,7 +140,7 @@ def sort_tokens_backward(dxs, slot_pos, dx=None, stream=None):
     T, k, H, shape = _slots(dxs, slot_pos, "dxs")
     dx = _out(dx, (T, H), dxs.dtype, dxs, "dx")
     _check("moe_sort_tokens_backward", load().moe_sort_tokens_backward(
-        _ptr(dxs), _ptr(slot_pos, torch.int32, "slot_pos"), shape, _ptr(dx, dxs.dtype, "dx"), _stream(stream)))
+        _ptr(dxs), _ptr(slot_pos, _I32, "slot_pos"), shape, _ptr(dx, dxs.dtype, "dx"), _stream(stream)))
     return dx
 
 
@@ -136,7 +152,7 @@ def return_tokens(ys, slot_pos, topk_w, shared=None, out=None, stream=None):
     _shaped(shared, (T, H), "shared")
     out = _out(out, (T, H), ys.dtype, ys, "out")
     _check("moe_return_tokens", load().moe_return_tokens(
-        _ptr(ys), _ptr(slot_pos, torch.int32, "slot_pos"), _ptr(topk_w, torch.float32, "topk_w"),
+        _ptr(ys), _ptr(slot_pos, _I32, "slot_pos"), _ptr(topk_w, _F32, "topk_w"),
         _ptr(shared, ys.dtype, "shared"), shape, _ptr(out, ys.dtype, "out"), _stream(stream)))
     return out
 
@@ -147,10 +163,10 @@ def return_tokens_backward(dout, ys, slot_pos, topk_w, dys=None, dw=None, stream
     _shaped(dout, (T, H), "dout")
     _shaped(topk_w, (T, k), "topk_w")
     dys = _out(dys, (T * k, H), ys.dtype, ys, "dys")
-    dw = _out(dw, (T, k), torch.float32, ys, "dw")
+    dw = _out(dw, (T, k), _F32, ys, "dw")
     _check("moe_return_tokens_backward", load().moe_return_tokens_backward(
-        _ptr(dout, ys.dtype, "dout"), _ptr(ys), _ptr(slot_pos, torch.int32, "slot_pos"),
-        _ptr(topk_w, torch.float32, "topk_w"), shape, _ptr(dys, ys.dtype, "dys"), _ptr(dw, torch.float32, "dw"),
+        _ptr(dout, ys.dtype, "dout"), _ptr(ys), _ptr(slot_pos, _I32, "slot_pos"),
+        _ptr(topk_w, _F32, "topk_w"), shape, _ptr(dys, ys.dtype, "dys"), _ptr(dw, _F32, "dw"),
         _stream(stream)))
     return dys, dw
 
@@ -167,7 +183,7 @@ class BlockFP8Weights:
     def c(self) -> MoeBlockFp8Weights:
         G, N, K = self.codes.shape
         _shaped(self.scales, (G, -(-N // 128), -(-K // 128)), "scales")
-        return MoeBlockFp8Weights(_ptr(self.codes, torch.uint8, "codes"), _ptr(self.scales, torch.float32, "scales"), G, N, K)
+        return MoeBlockFp8Weights(_ptr(self.codes, _U8, "codes"), _ptr(self.scales, _F32, "scales"), G, N, K)
 
 
 def quantize_block_fp8(w: torch.Tensor, stream=None) -> BlockFP8Weights:
@@ -196,7 +212,7 @@ def quantize_rows_block_fp8(x: torch.Tensor, stream=None):
     codes = torch.empty(rows, 128 * KB, dtype=torch.uint8, device=x.device)
     scales = torch.empty(rows, -(-KB // 4) * 4, dtype=torch.float32, device=x.device)
     _check("moe_quantize_rows_block_fp8", load().moe_quantize_rows_block_fp8(
-        _ptr(x, torch.bfloat16, "x"), rows, K, _ptr(codes), _ptr(scales), _stream(stream)))
+        _ptr(x, _BF16, "x"), rows, K, _ptr(codes), _ptr(scales), _stream(stream)))
     return codes, scales
 
 
@@ -219,8 +235,8 @@ def block_fp8_matmul(x, w: BlockFP8Weights, ws, offsets=None, out=None, out_fp32
         out = torch.empty(M, N, dtype=torch.float32 if out_fp32 else torch.bfloat16, device=x.device)
     _shaped(out, (M, N), "out")
     _check("moe_block_fp8_matmul", load().moe_block_fp8_matmul(
-        _ptr(x, torch.bfloat16, "x"), M, _ptr(offsets, torch.int32, "offsets"), w.c(), _ptr(out), _row_type(out, "out"),
-        _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+        _ptr(x, _BF16, "x"), M, _ptr(offsets, _I32, "offsets"), w.c(), _ptr(out), _row_type(out, "out"),
+        _ptr(ws, _U8, "ws"), ws.numel(), _stream(stream)))
     return out
 
 
@@ -236,41 +252,43 @@ def _gate(gate, T, H):
     is per channel; pass [T, 1] for one per token."""
     if gate is None:
         return GATE_NONE, None
-    shape = tuple(gate.shape)
+    shape = gate.shape
     if shape == (H,):
         return GATE_CHANNEL, torch.float32
     if shape in ((T,), (T, 1)):
         return GATE_TOKEN, torch.float32
     if shape == (T, H):
         return GATE_ELEMENT, torch.bfloat16
-    raise ValueError(f"gate must have shape ({H},), ({T},), ({T}, 1) or ({T}, {H}), got {shape}")
+    raise ValueError(f"gate must have shape ({H},), ({T},), ({T}, 1) or ({T}, {H}), got {tuple(shape)}")
 
 
 def norm_before(x, weight, eps: float = 1e-6, weight_offset: float = 0.0, n=None, rstd=None, stream=None):
     """(n bf16 [T, H], rstd fp32 [T]) of x [T, H] (bf16 or fp32): n = x rstd (weight + weight_offset)."""
     T, H = x.shape
     _shaped(weight, (H,), "weight")
-    n = _out(n, (T, H), torch.bfloat16, x, "n")
-    rstd = _out(rstd, (T,), torch.float32, x, "rstd")
+    n = _out(n, (T, H), _BF16, x, "n")
+    rstd = _out(rstd, (T,), _F32, x, "rstd")
     _check("moe_norm_before", load().moe_norm_before(
-        _ptr(x), _ptr(weight, torch.float32, "weight"),
-        MoeNorm(T, H, _row_type(x, "x"), 0, GATE_NONE, eps, weight_offset, 1.0, 1.0), _ptr(n, torch.bfloat16, "n"),
-        _ptr(rstd, torch.float32, "rstd"), _stream(stream)))
+        _ptr(x), _ptr(weight, _F32, "weight"),
+        MoeNorm(T, H, _row_type(x, "x"), 0, GATE_NONE, eps, weight_offset, 1.0, 1.0), _ptr(n, _BF16, "n"),
+        _ptr(rstd, _F32, "rstd"), _stream(stream)))
     return n, rstd
 
 
 def norm_before_backward(dn, x, weight, rstd, ws, dresidual=None, weight_offset: float = 0.0, dx=None, dw=None, stream=None):
     """(dx, dw) of norm_before; dresidual (x's type) is added to dx."""
     T, H = x.shape
-    for t, shape, name in ((dn, (T, H), "dn"), (weight, (H,), "weight"), (rstd, (T,), "rstd"), (dresidual, (T, H), "dresidual")):
-        _shaped(t, shape, name)
-    f32 = torch.float32
+    rows, cols, f32 = x.shape, (H,), _F32
+    _shaped(dn, rows, "dn")
+    _shaped(weight, cols, "weight")
+    _shaped(rstd, (T,), "rstd")
+    _shaped(dresidual, rows, "dresidual")
     dx = _out(dx, (T, H), x.dtype, x, "dx")
     dw = _out(dw, (H,), f32, x, "dw")
     _check("moe_norm_before_backward", load().moe_norm_before_backward(
-        _ptr(dn, torch.bfloat16, "dn"), _ptr(x), _ptr(weight, f32, "weight"), _ptr(rstd, f32, "rstd"),
+        _ptr(dn, _BF16, "dn"), _ptr(x), _ptr(weight, f32, "weight"), _ptr(rstd, f32, "rstd"),
         _ptr(dresidual, x.dtype, "dresidual"), MoeNorm(T, H, _row_type(x, "x"), 0, GATE_NONE, 0.0, weight_offset, 1.0, 1.0),
-        _ptr(dx, x.dtype, "dx"), _ptr(dw, f32, "dw"), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+        _ptr(dx, x.dtype, "dx"), _ptr(dw, f32, "dw"), _ptr(ws, _U8, "ws"), ws.numel(), _stream(stream)))
     return dx, dw
 
 
@@ -280,20 +298,21 @@ def norm_after(y, x, weight, gate=None, w_next=None, residual_scale: float = 1.0
     n of the stored out: (out, n or None, rstd, rstd_next or None)."""
     T, H = x.shape
     kind, gate_type = _gate(gate, T, H)
-    for t, shape, name in ((y, (T, H), "y"), (weight, (H,), "weight"), (w_next, (H,), "w_next")):
-        _shaped(t, shape, name)
-    f32 = torch.float32
+    rows, cols, f32 = x.shape, (H,), _F32
+    _shaped(y, rows, "y")
+    _shaped(weight, cols, "weight")
+    _shaped(w_next, cols, "w_next")
     out = _out(out, (T, H), x.dtype, x, "out")
     rstd = _out(rstd, (T,), f32, x, "rstd")
     if w_next is not None:
-        n = _out(n, (T, H), torch.bfloat16, x, "n")
+        n = _out(n, (T, H), _BF16, x, "n")
         rstd_next = _out(rstd_next, (T,), f32, x, "rstd_next")
     elif n is not None or rstd_next is not None:
         raise ValueError("n and rstd_next are outputs of the next norm: they need w_next")
     _check("moe_norm_after", load().moe_norm_after(
         _ptr(y), _ptr(x), _ptr(weight, f32, "weight"), _ptr(gate, gate_type, "gate"), _ptr(w_next, f32, "w_next"),
         MoeNorm(T, H, _row_type(x, "x"), _row_type(y, "y"), kind, eps, weight_offset, residual_scale, branch_scale),
-        _ptr(out, x.dtype, "out"), _ptr(n, torch.bfloat16, "n"), _ptr(rstd, f32, "rstd"), _ptr(rstd_next, f32, "rstd_next"),
+        _ptr(out, x.dtype, "out"), _ptr(n, _BF16, "n"), _ptr(rstd, f32, "rstd"), _ptr(rstd_next, f32, "rstd_next"),
         _stream(stream)))
     return out, n, rstd, rstd_next
 
@@ -308,10 +327,13 @@ def norm_after_backward(dout, y, weight, rstd, ws, gate=None, dn=None, out=None,
     nexts = (dn, out, w_next, rstd_next)
     if any(t is None for t in nexts) and any(t is not None for t in nexts):
         raise ValueError("dn, out, w_next and rstd_next belong to the next norm: give all of them or none")
-    for t, shape, name in ((dout, (T, H), "dout"), (weight, (H,), "weight"), (rstd, (T,), "rstd"), (dn, (T, H), "dn"),
-                           (out, (T, H), "out"), (w_next, (H,), "w_next"), (rstd_next, (T,), "rstd_next")):
-        _shaped(t, shape, name)
-    f32 = torch.float32
+    rows, cols, f32 = y.shape, (H,), _F32
+    for t, name in ((dout, "dout"), (dn, "dn"), (out, "out")):
+        _shaped(t, rows, name)
+    _shaped(weight, cols, "weight")
+    _shaped(w_next, cols, "w_next")
+    _shaped(rstd, (T,), "rstd")
+    _shaped(rstd_next, (T,), "rstd_next")
     dy = _out(dy, (T, H), y.dtype, y, "dy")
     dx = _out(dx, (T, H), dout.dtype, dout, "dx")
     dw = _out(dw, (H,), f32, y, "dw")
@@ -322,11 +344,11 @@ def norm_after_backward(dout, y, weight, rstd, ws, gate=None, dn=None, out=None,
     if (gate is None and dgate is not None) or (w_next is None and dw_next is not None):
         raise ValueError("dgate needs gate, dw_next needs w_next")
     _check("moe_norm_after_backward", load().moe_norm_after_backward(
-        _ptr(dout), _ptr(dn, torch.bfloat16, "dn"), _ptr(y), _ptr(out, dout.dtype, "out"), _ptr(weight, f32, "weight"),
+        _ptr(dout), _ptr(dn, _BF16, "dn"), _ptr(y), _ptr(out, dout.dtype, "out"), _ptr(weight, f32, "weight"),
         _ptr(gate, gate_type, "gate"), _ptr(w_next, f32, "w_next"), _ptr(rstd, f32, "rstd"), _ptr(rstd_next, f32, "rstd_next"),
         MoeNorm(T, H, _row_type(dout, "dout"), _row_type(y, "y"), kind, 0.0, weight_offset, residual_scale, branch_scale),
         _ptr(dy, y.dtype, "dy"), _ptr(dx, dout.dtype, "dx"), _ptr(dw, f32, "dw"), _ptr(dgate, gate_type, "dgate"),
-        _ptr(dw_next, f32, "dw_next"), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)))
+        _ptr(dw_next, f32, "dw_next"), _ptr(ws, _U8, "ws"), ws.numel(), _stream(stream)))
     return dy, dx, dw, dgate, dw_next
 
 

@@ -7,9 +7,11 @@
 // Gradients (xh = rstd x):  dx of a norm = rstd (d - xh mean(d xh)) with d = dn w',  dw = sum_t dn xh.
 // Rows are read once and stay in registers between the row sums and their use, so every call moves
 // the bytes of its inputs and outputs once and is bound by HBM; weights and gates of a channel stay
-// in registers over the rows that a CTA takes.  Sums are fp32 in a fixed order: a row's by
-// shuffles and one array per CTA, a column's in registers over the CTA's rows, written per CTA and
-// summed by a second kernel (no atomics).
+// in registers over the rows that a thread takes.  A group of threads takes a row (one or two units
+// of eight elements per thread), a CTA several groups, and a group's next row is loaded before the
+// current one's sums, whose barriers it would otherwise wait behind.  Sums are fp32 in a fixed
+// order: a row's by shuffles and one array per group, a column's in registers over the group's
+// rows, then over the CTA's groups, written per CTA and summed by a second kernel (no atomics).
 #include <algorithm>
 
 #include "row_units.cuh"
@@ -31,26 +33,43 @@ struct NormArgs {
   float* part;                 // [sums][grid][H] column sums of each CTA
 };
 
-// Sums of up to two values over the block, the same bits in every thread.  `slot` alternates
-// between calls, so one barrier per call is enough.
+// This thread's place: rows are taken by groups of blockDim.x threads, threadIdx.y is the group.
+// Units of a row: threadIdx.x, threadIdx.x + blockDim.x.
+struct Place {
+  int64_t row, stride;
+  __device__ __forceinline__ Place()
+      : row(static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y), stride(static_cast<int64_t>(gridDim.x) * blockDim.y) {}
+};
+
+// Sums of N values over the group, the same bits in every thread of it.  `slot` alternates between
+// calls, so one barrier per call is enough.
+constexpr int kMaxWarps = 32;
 template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], int& slot) {
-  __shared__ float s_sum[2][2][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+__device__ __forceinline__ void group_sum(float (&v)[N], int& slot) {
+  __shared__ __align__(16) float s_sum[2][N][kMaxWarps];
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+  const int warps = blockDim.x >> 5;
   if (warps == 1) return;
-  if (lane == 0)
+  const int first = threadIdx.y * warps, warp = first + (threadIdx.x >> 5);   // groups of more than one warp have 2 or a multiple of 4
+  if ((threadIdx.x & 31) == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) s_sum[slot][i][warp] = v[i];
-  __syncthreads();
+  asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float t = lane < warps ? s_sum[slot][i][lane] : 0.0f;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
+    const float* p = &s_sum[slot][i][first];
+    float t = 0.0f;
+    if (warps == 2) {
+      t = p[0] + p[1];
+    } else {
+      for (int w = 0; w < warps; w += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(p + w);
+        t += (q.x + q.y) + (q.z + q.w);
+      }
+    }
     v[i] = t;
   }
   slot ^= 1;
@@ -68,21 +87,23 @@ __device__ __forceinline__ void load_vec(const float* p, int u, float add, float
 #define EACH_UNIT(i) _Pragma("unroll") for (int i = 0; i < U; ++i) if (UNIT(i) < a.units)
 #define EACH(c) _Pragma("unroll") for (int c = 0; c < 8; ++c)
 
-template <typename R, int U, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) norm_before_kernel(NormArgs a) {
+template <typename R, int U, int kMaxThreads, int kPerSm>
+__global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_before_kernel(NormArgs a) {
   float w[U][8];
+  Unit8<R> qx[U];
   int slot = 0;
+  const Place at;
   pdl_wait();
+  if (at.row < a.T) EACH_UNIT(i) qx[i].load(a.x, at.row * a.units + UNIT(i));
   EACH_UNIT(i) load_vec(a.w, UNIT(i), a.w_off, w[i]);
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  for (int64_t t = at.row; t < a.T; t += at.stride) {
     float x[U][8], sum[1] = {0.0f};
     EACH_UNIT(i) {
-      Unit8<R> q;
-      q.load(a.x, t * a.units + UNIT(i));
-      q.get(x[i]);
+      qx[i].get(x[i]);
+      if (t + at.stride < a.T) qx[i].load(a.x, (t + at.stride) * a.units + UNIT(i));
       EACH(c) sum[0] = fmaf(x[i][c], x[i][c], sum[0]);
     }
-    block_sum(sum, slot);
+    group_sum(sum, slot);
     const float rstd = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rstd;
     EACH_UNIT(i) {
@@ -105,27 +126,36 @@ __device__ __forceinline__ void gate_of(const NormArgs& a, int64_t t, int u, con
   }
 }
 
-template <typename R, typename Y, int U, int kMaxThreads, bool kNext>
-__global__ void __launch_bounds__(kMaxThreads) norm_after_kernel(NormArgs a) {
+template <typename R, typename Y, int U, int kMaxThreads, int kPerSm, bool kNext>
+__global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_after_kernel(NormArgs a) {
   float w[U][8], gc[U][8], wn[U][8];
+  Unit8<Y> qy[U];
+  Unit8<R> qx[U];
   int slot = 0;
+  const Place at;
+  auto load_row = [&](int64_t t) {
+    EACH_UNIT(i) {
+      qy[i].load(a.y, t * a.units + UNIT(i));
+      qx[i].load(a.x, t * a.units + UNIT(i));
+    }
+  };
   pdl_wait();
+  if (at.row < a.T) load_row(at.row);
   EACH_UNIT(i) {
     load_vec(a.w, UNIT(i), a.w_off, w[i]);
     if (kNext) load_vec(a.w_next, UNIT(i), a.w_off, wn[i]);
     if (a.gate_kind == MOE_GATE_CHANNEL) load_vec(static_cast<const float*>(a.gate), UNIT(i), 0.0f, gc[i]);
   }
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  for (int64_t t = at.row; t < a.T; t += at.stride) {
     float y[U][8], sum[1] = {0.0f};
     Unit8<R> x[U];
     EACH_UNIT(i) {
-      Unit8<Y> q;
-      q.load(a.y, t * a.units + UNIT(i));
-      x[i].load(a.x, t * a.units + UNIT(i));
-      q.get(y[i]);
+      qy[i].get(y[i]);
+      x[i] = qx[i];
       EACH(c) sum[0] = fmaf(y[i][c], y[i][c], sum[0]);
     }
-    block_sum(sum, slot);
+    if (t + at.stride < a.T) load_row(t + at.stride);
+    group_sum(sum, slot);
     const float rstd = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rstd;
     const float gt = a.gate_kind == MOE_GATE_TOKEN ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
@@ -144,7 +174,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_after_kernel(NormArgs a) {
       }
     }
     if (kNext) {
-      block_sum(sum, slot);
+      group_sum(sum, slot);
       const float rn = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
       if (threadIdx.x == 0 && a.rstd_next) a.rstd_next[t] = rn;
       EACH_UNIT(i) {
@@ -157,8 +187,25 @@ __global__ void __launch_bounds__(kMaxThreads) norm_after_kernel(NormArgs a) {
   }
 }
 
+// Adds the groups' column sums in group order (through shared memory) and writes the CTA's row.
 template <int U>
-__device__ __forceinline__ void write_part(const NormArgs& a, int which, const float (&s)[U][8]) {
+__device__ __forceinline__ void write_part(const NormArgs& a, int which, float (&s)[U][8], float* s_cols) {
+  float4* mine = reinterpret_cast<float4*>(s_cols) + ((threadIdx.y - 1) * blockDim.x + threadIdx.x) * 2;
+  if (blockDim.y > 1) {                 // one unit per thread then
+    __syncthreads();
+    if (threadIdx.y > 0) {
+      mine[0] = make_float4(s[0][0], s[0][1], s[0][2], s[0][3]);
+      mine[1] = make_float4(s[0][4], s[0][5], s[0][6], s[0][7]);
+    }
+    __syncthreads();
+  }
+  if (threadIdx.y > 0) return;
+  for (int g = 1; g < static_cast<int>(blockDim.y); ++g) {
+    const float4* q = reinterpret_cast<const float4*>(s_cols) + ((g - 1) * blockDim.x + threadIdx.x) * 2;
+    const float4 lo = q[0], hi = q[1];
+    s[0][0] += lo.x; s[0][1] += lo.y; s[0][2] += lo.z; s[0][3] += lo.w;
+    s[0][4] += hi.x; s[0][5] += hi.y; s[0][6] += hi.z; s[0][7] += hi.w;
+  }
   float* row = a.part + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.units * 8;
   EACH_UNIT(i) {
     Unit8<float> q;
@@ -167,27 +214,39 @@ __device__ __forceinline__ void write_part(const NormArgs& a, int which, const f
   }
 }
 
+constexpr int kGradThreads = 512;       // threads of a gradient's CTA, groups of fewer than that together
+
 template <typename R, int U, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) norm_before_grad_kernel(NormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_before_grad_kernel(NormArgs a) {
+  __shared__ __align__(16) float s_cols[kGradThreads * 8];
   float w[U][8], dw[U][8];
+  Unit8<R> qx[U], qr[U];
+  Unit8<uint16_t> qd[U];
+  float q_rstd = 0.0f;
   int slot = 0;
+  const Place at;
+  auto load_row = [&](int64_t t) {
+    EACH_UNIT(i) {
+      qx[i].load(a.x, t * a.units + UNIT(i));
+      qd[i].load(a.dn, t * a.units + UNIT(i));
+      if (a.dres) qr[i].load(a.dres, t * a.units + UNIT(i));
+    }
+    q_rstd = __ldg(a.rstd_in + t);
+  };
   pdl_wait();
+  if (at.row < a.T) load_row(at.row);
   EACH_UNIT(i) {
     load_vec(a.w, UNIT(i), a.w_off, w[i]);
     EACH(c) dw[i][c] = 0.0f;
   }
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const float rstd = __ldg(a.rstd_in + t);
+  for (int64_t t = at.row; t < a.T; t += at.stride) {
+    const float rstd = q_rstd;
     float xh[U][8], d[U][8], dot[1] = {0.0f};
     Unit8<R> res[U];
     EACH_UNIT(i) {
-      Unit8<R> qx;
-      Unit8<uint16_t> qd;
-      qx.load(a.x, t * a.units + UNIT(i));
-      qd.load(a.dn, t * a.units + UNIT(i));
-      if (a.dres) res[i].load(a.dres, t * a.units + UNIT(i));
-      qx.get(xh[i]);
-      qd.get(d[i]);
+      qx[i].get(xh[i]);
+      qd[i].get(d[i]);
+      res[i] = qr[i];
       EACH(c) {
         xh[i][c] *= rstd;
         dw[i][c] = fmaf(d[i][c], xh[i][c], dw[i][c]);
@@ -195,7 +254,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_before_grad_kernel(NormArgs 
         dot[0] = fmaf(d[i][c], xh[i][c], dot[0]);
       }
     }
-    block_sum(dot, slot);
+    if (t + at.stride < a.T) load_row(t + at.stride);
+    group_sum(dot, slot);
     const float m = dot[0] * a.inv_h;
     EACH_UNIT(i) {
       float r[8];
@@ -207,16 +267,36 @@ __global__ void __launch_bounds__(kMaxThreads) norm_before_grad_kernel(NormArgs 
       q.store(a.dx, t * a.units + UNIT(i));
     }
   }
-  write_part<U>(a, 0, dw);
+  write_part<U>(a, 0, dw, s_cols);
 }
 
 // Gradient of `after`: with d = dout (+ the gradient that comes through the next norm, whose input
 // is the stored out),  dx = a d,  dgate = b d rms(y) w',  and the norm's gradient of b d g.
 template <typename R, typename Y, int U, int kMaxThreads, bool kNext>
-__global__ void __launch_bounds__(kMaxThreads) norm_after_grad_kernel(NormArgs a) {
+__global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArgs a) {
+  __shared__ __align__(16) float s_cols[kGradThreads * 8];
   float dw[U][8], dwn[U][8], dg[U][8];
+  Unit8<R> qd[U], qo[U];
+  Unit8<Y> qy[U];
+  Unit8<uint16_t> qn[U];
+  float q_rstd = 0.0f, q_rn = 0.0f;
   int slot = 0;
+  const Place at;
+  auto load_row = [&](int64_t t) {
+    EACH_UNIT(i) {
+      const int64_t u = t * a.units + UNIT(i);
+      qd[i].load(a.dout, u);
+      qy[i].load(a.y, u);
+      if (kNext) {
+        qo[i].load(a.x, u);
+        qn[i].load(a.dn, u);
+      }
+    }
+    q_rstd = __ldg(a.rstd_in + t);
+    if (kNext) q_rn = __ldg(a.rstd_next_in + t);
+  };
   pdl_wait();
+  if (at.row < a.T) load_row(at.row);
   EACH_UNIT(i) {
     EACH(c) {
       dw[i][c] = 0.0f;
@@ -224,28 +304,17 @@ __global__ void __launch_bounds__(kMaxThreads) norm_after_grad_kernel(NormArgs a
       dg[i][c] = 0.0f;
     }
   }
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const float rstd = __ldg(a.rstd_in + t);
-    float d[U][8];
-    Unit8<Y> qy[U];
+  for (int64_t t = at.row; t < a.T; t += at.stride) {
+    const float rstd = q_rstd, rn = q_rn;
+    float d[U][8], yh[U][8], oh[U][8], e[U][8], dot[1] = {0.0f};
     EACH_UNIT(i) {
-      Unit8<R> q;
-      q.load(a.dout, t * a.units + UNIT(i));
-      qy[i].load(a.y, t * a.units + UNIT(i));
-      q.get(d[i]);
-    }
-    if (kNext) {
-      const float rn = __ldg(a.rstd_next_in + t);
-      float oh[U][8], e[U][8], dot[1] = {0.0f};
-      EACH_UNIT(i) {
-        Unit8<R> qo;
-        Unit8<uint16_t> qn;
+      qd[i].get(d[i]);
+      qy[i].get(yh[i]);
+      if (kNext) {
         float wn[8];
-        qo.load(a.x, t * a.units + UNIT(i));
-        qn.load(a.dn, t * a.units + UNIT(i));
         load_vec(a.w_next, UNIT(i), a.w_off, wn);
-        qo.get(oh[i]);
-        qn.get(e[i]);
+        qo[i].get(oh[i]);
+        qn[i].get(e[i]);
         EACH(c) {
           oh[i][c] *= rn;
           dwn[i][c] = fmaf(e[i][c], oh[i][c], dwn[i][c]);
@@ -253,19 +322,21 @@ __global__ void __launch_bounds__(kMaxThreads) norm_after_grad_kernel(NormArgs a
           dot[0] = fmaf(e[i][c], oh[i][c], dot[0]);
         }
       }
-      block_sum(dot, slot);
+    }
+    if (t + at.stride < a.T) load_row(t + at.stride);
+    if (kNext) {
+      group_sum(dot, slot);
       const float m = dot[0] * a.inv_h;
       EACH_UNIT(i) EACH(c) d[i][c] += rn * (e[i][c] - oh[i][c] * m);
     }
     const float gt = a.gate_kind == MOE_GATE_TOKEN ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
-    float yh[U][8], sums[2] = {0.0f, 0.0f};
+    float sums[2] = {0.0f, 0.0f};
     EACH_UNIT(i) {
       float r[8], g[8], w[8];
       EACH(c) r[c] = a.a * d[i][c];
       Unit8<R> q;
       q.set(r);
       q.store(a.dx, t * a.units + UNIT(i));
-      qy[i].get(yh[i]);
       load_vec(a.w, UNIT(i), a.w_off, w);
       float gc[8];
       if (a.gate_kind == MOE_GATE_CHANNEL) load_vec(static_cast<const float*>(a.gate), UNIT(i), 0.0f, gc);
@@ -287,7 +358,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_after_grad_kernel(NormArgs a
         qg.store(a.dgate, t * a.units + UNIT(i));
       }
     }
-    block_sum(sums, slot);
+    group_sum(sums, slot);
     if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(a.dgate)[t] = sums[1];
     const float m = sums[0] * a.inv_h;
     EACH_UNIT(i) {
@@ -297,9 +368,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_after_grad_kernel(NormArgs a
       q.store(a.dy, t * a.units + UNIT(i));
     }
   }
-  write_part<U>(a, 0, dw);
-  if (kNext) write_part<U>(a, 1, dwn);
-  if (a.gate_kind == MOE_GATE_CHANNEL) write_part<U>(a, 2, dg);
+  write_part<U>(a, 0, dw, s_cols);
+  if (kNext) write_part<U>(a, 1, dwn, s_cols);
+  if (a.gate_kind == MOE_GATE_CHANNEL) write_part<U>(a, 2, dg, s_cols);
 }
 
 // Column sums: part [3][rows][H] -> one vector each (NULL: skipped).  32 columns per CTA, 32
@@ -324,18 +395,30 @@ __global__ void __launch_bounds__(1024) norm_columns_kernel(const float* __restr
 }
 
 constexpr int kOneUnit = 512;    // rows of up to this many units: one unit per thread, else two
+constexpr int kForwardThreads = 256;
+constexpr int kMaxSms = 160;     // the workspace holds the column sums of this many CTAs
 
-dim3 block_of(int units) {
+// Threads of a row: 32, 64 or a multiple of 128.
+int row_threads(int units) {
   const int per = units <= kOneUnit ? units : (units + 1) / 2;
-  return dim3((per + 31) / 32 * 32);
+  return per <= 32 ? 32 : per <= 64 ? 64 : (per + 127) / 128 * 128;
 }
 
-// CTAs of a launch: as many as are resident (about 1024 threads per SM), one row each at least.
-// The workspace holds the column sums of kMaxSms such SMs.
-constexpr int kMaxSms = 160;
-int grid_of(int64_t T, int units, int n_sm) {
-  const int per_sm = std::max(1, 1024 / static_cast<int>(block_of(units).x));
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(T, static_cast<int64_t>(std::min(n_sm, kMaxSms)) * per_sm)));
+// A launch of as many CTAs as are resident (`per_sm`), with a row per group at least.
+struct NormLaunch {
+  dim3 grid, block;
+};
+NormLaunch launch_of(int64_t T, int units, int threads, int per_sm, int n_sm) {
+  const int x = row_threads(units), y = std::max(1, threads / x);
+  const int64_t most = static_cast<int64_t>(n_sm) * std::max(1, per_sm * threads / (x * y));
+  NormLaunch l;
+  l.block = dim3(x, y);
+  l.grid = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min((T + y - 1) / y, most))));
+  return l;
+}
+NormLaunch forward_launch(int64_t T, int units, int n_sm) { return launch_of(T, units, kForwardThreads, 4, n_sm); }
+NormLaunch grad_launch(int64_t T, int units, int n_sm) {
+  return launch_of(T, units, kGradThreads, 1, std::min(n_sm, kMaxSms));
 }
 
 NormArgs args_of(const moe_norm_t& s) {
@@ -351,18 +434,25 @@ NormArgs args_of(const moe_norm_t& s) {
   return a;
 }
 
-#define PICK_U(K, ...) (s.H / 8 <= kOneUnit ? K<__VA_ARGS__, 1, 512> : K<__VA_ARGS__, 2, 1024>)
-#define PICK_U_NEXT(K, next, ...)                                                              \
-  (s.H / 8 <= kOneUnit ? ((next) ? K<__VA_ARGS__, 1, 512, true> : K<__VA_ARGS__, 1, 512, false>) \
-                       : ((next) ? K<__VA_ARGS__, 2, 1024, true> : K<__VA_ARGS__, 2, 1024, false>))
-#define PICK_RY(K, next)                                                                                      \
-  (s.residual_fp32 ? (s.branch_fp32 ? PICK_U_NEXT(K, next, float, float) : PICK_U_NEXT(K, next, float, uint16_t)) \
-                   : (s.branch_fp32 ? PICK_U_NEXT(K, next, uint16_t, float) : PICK_U_NEXT(K, next, uint16_t, uint16_t)))
+// Launch bounds: up to 256 threads four CTAs per SM (64 registers), else one CTA; two units per
+// thread in up to 512 threads (128 registers), and in 1024 (64, some spilled) above 8192 columns.
+#define PICK_UNITS(small, one, two, more) \
+  (s.H / 8 <= 256 ? small : s.H / 8 <= kOneUnit ? one : s.H / 8 <= 2 * kOneUnit ? two : more)
+#define PICK_BEFORE(K, R) PICK_UNITS((K<R, 1, 256, 4>), (K<R, 1, 512, 1>), (K<R, 2, 512, 1>), (K<R, 2, 1024, 1>))
+#define PICK_GRAD(K, R) PICK_UNITS((K<R, 1, 512>), (K<R, 1, 512>), (K<R, 2, 512>), (K<R, 2, 1024>))
+#define PICK_AFTER(K, R, Y, next) \
+  PICK_UNITS((K<R, Y, 1, 256, 4, next>), (K<R, Y, 1, 512, 1, next>), (K<R, Y, 2, 512, 1, next>), (K<R, Y, 2, 1024, 1, next>))
+#define PICK_AFTER_GRAD(K, R, Y, next) \
+  PICK_UNITS((K<R, Y, 1, 512, next>), (K<R, Y, 1, 512, next>), (K<R, Y, 2, 512, next>), (K<R, Y, 2, 1024, next>))
+#define PICK_NEXT(PICK, K, R, Y) (next ? PICK(K, R, Y, true) : PICK(K, R, Y, false))
+#define PICK_TYPES(PICK, K)                                                                                          \
+  (s.residual_fp32 ? (s.branch_fp32 ? PICK_NEXT(PICK, K, float, float) : PICK_NEXT(PICK, K, float, uint16_t))        \
+                   : (s.branch_fp32 ? PICK_NEXT(PICK, K, uint16_t, float) : PICK_NEXT(PICK, K, uint16_t, uint16_t)))
 
 }  // namespace
 
 // CTAs that write column sums, at most (the size of the workspace).
-int64_t norm_max_parts(int64_t T, int H) { return grid_of(T, H / 8, kMaxSms); }
+int64_t norm_max_parts(int64_t T, int H) { return grad_launch(T, H / 8, kMaxSms).grid.x; }
 
 cudaError_t launch_norm_before(const moe_norm_t& s, const void* x, const float* w, void* n, float* rstd, cudaStream_t st) {
   int n_sm = 0;
@@ -373,8 +463,9 @@ cudaError_t launch_norm_before(const moe_norm_t& s, const void* x, const float* 
   a.w = w;
   a.n = n;
   a.rstd = rstd;
-  auto kern = s.residual_fp32 ? PICK_U(norm_before_kernel, float) : PICK_U(norm_before_kernel, uint16_t);
-  return launch_pdl(true, kern, dim3(grid_of(s.T, a.units, n_sm)), block_of(a.units), 0, st, a);
+  auto kern = s.residual_fp32 ? PICK_BEFORE(norm_before_kernel, float) : PICK_BEFORE(norm_before_kernel, uint16_t);
+  const NormLaunch l = forward_launch(s.T, a.units, n_sm);
+  return launch_pdl(true, kern, l.grid, l.block, 0, st, a);
 }
 
 cudaError_t launch_norm_after(const moe_norm_t& s, const void* y, const void* x, const float* w, const void* gate,
@@ -392,8 +483,10 @@ cudaError_t launch_norm_after(const moe_norm_t& s, const void* y, const void* x,
   a.n = n;
   a.rstd = rstd;
   a.rstd_next = rstd_next;
-  auto kern = PICK_RY(norm_after_kernel, w_next != nullptr);
-  return launch_pdl(true, kern, dim3(grid_of(s.T, a.units, n_sm)), block_of(a.units), 0, st, a);
+  const bool next = w_next != nullptr;
+  auto kern = PICK_TYPES(PICK_AFTER, norm_after_kernel);
+  const NormLaunch l = forward_launch(s.T, a.units, n_sm);
+  return launch_pdl(true, kern, l.grid, l.block, 0, st, a);
 }
 
 cudaError_t launch_norm_before_grad(const moe_norm_t& s, const void* dn, const void* x, const float* w, const float* rstd,
@@ -409,9 +502,10 @@ cudaError_t launch_norm_before_grad(const moe_norm_t& s, const void* dn, const v
   a.dres = dres;
   a.dx = dx;
   a.part = part;
-  const int grid = grid_of(s.T, a.units, n_sm);
-  auto kern = s.residual_fp32 ? PICK_U(norm_before_grad_kernel, float) : PICK_U(norm_before_grad_kernel, uint16_t);
-  e = launch_pdl(true, kern, dim3(grid), block_of(a.units), 0, st, a);
+  const NormLaunch l = grad_launch(s.T, a.units, n_sm);
+  const int grid = static_cast<int>(l.grid.x);
+  auto kern = s.residual_fp32 ? PICK_GRAD(norm_before_grad_kernel, float) : PICK_GRAD(norm_before_grad_kernel, uint16_t);
+  e = launch_pdl(true, kern, l.grid, l.block, 0, st, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(true, norm_columns_kernel, dim3((s.H + 31) / 32, 1), dim3(1024), 0, st,
                     static_cast<const float*>(part), grid, s.H, dw, static_cast<float*>(nullptr),
@@ -439,9 +533,11 @@ cudaError_t launch_norm_after_grad(const moe_norm_t& s, const void* dout, const 
   a.dx = dx;
   a.dgate = dgate;
   a.part = part;
-  const int grid = grid_of(s.T, a.units, n_sm);
-  auto kern = PICK_RY(norm_after_grad_kernel, w_next != nullptr);
-  e = launch_pdl(true, kern, dim3(grid), block_of(a.units), 0, st, a);
+  const NormLaunch l = grad_launch(s.T, a.units, n_sm);
+  const int grid = static_cast<int>(l.grid.x);
+  const bool next = w_next != nullptr;
+  auto kern = PICK_TYPES(PICK_AFTER_GRAD, norm_after_grad_kernel);
+  e = launch_pdl(true, kern, l.grid, l.block, 0, st, a);
   if (e != cudaSuccess) return e;
   float* dgc = s.gate == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
   return launch_pdl(true, norm_columns_kernel, dim3((s.H + 31) / 32, dgc ? 3 : dw_next ? 2 : 1), dim3(1024), 0, st,
