@@ -5,6 +5,10 @@
 //                                          none, per channel, per token or per element)
 //           n'  = rms(out) w_next'        optionally, the next block's norm of the stored stream
 // Gradients (xh = rstd x):  dx of a norm = rstd (d - xh mean(d xh)) with d = dn w',  dw = sum_t dn xh.
+// Through the fused next norm and the branch this takes sums over a row of three products that do
+// not depend on one another (see norm_after_grad_kernel), so a row has one reduction; and the
+// gradients of the branch norm's weight and of a channel gate are one column sum, times b g and
+// b w' at the end.
 // Rows are read once and stay in registers between the row sums and their use, so every call moves
 // the bytes of its inputs and outputs once and is bound by HBM; weights and gates of a channel stay
 // in registers over the rows that a thread takes.  A group of threads takes a row (one or two units
@@ -30,7 +34,7 @@ struct NormArgs {
   const float *rstd_in, *rstd_next_in;
   void *out, *n, *dx, *dy, *dgate;
   float *rstd, *rstd_next;
-  float* part;                 // [sums][grid][H] column sums of each CTA
+  float* part;                 // [2][grid][H] column sums of each CTA
 };
 
 // This thread's place: rows are taken by groups of blockDim.x threads, threadIdx.y is the group.
@@ -75,39 +79,42 @@ __device__ __forceinline__ void group_sum(float (&v)[N], int& slot) {
   slot ^= 1;
 }
 
-__device__ __forceinline__ void load_vec(const float* p, int u, float add, float (&f)[8]) {
+__device__ __forceinline__ Vec8 load_vec(const float* p, int u, float add) {
   Unit8<float> q;
   q.load(p, u);
-  q.get(f);
+  Vec8 v = q.get();
 #pragma unroll
-  for (int c = 0; c < 8; ++c) f[c] += add;
+  for (int c = 0; c < 4; ++c) v.p[c] = add2(v.p[c], both(add));
+  return v;
 }
 
 #define UNIT(i) (static_cast<int>(threadIdx.x) + (i) * static_cast<int>(blockDim.x))
 #define EACH_UNIT(i) _Pragma("unroll") for (int i = 0; i < U; ++i) if (UNIT(i) < a.units)
-#define EACH(c) _Pragma("unroll") for (int c = 0; c < 8; ++c)
+#define EACH(c) _Pragma("unroll") for (int c = 0; c < 4; ++c)
 
 template <typename R, int U, int kMaxThreads, int kPerSm>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_before_kernel(NormArgs a) {
-  float w[U][8];
+  Vec8 w[U];
   Unit8<R> qx[U];
   int slot = 0;
   const Place at;
   pdl_wait();
   if (at.row < a.T) EACH_UNIT(i) qx[i].load(a.x, at.row * a.units + UNIT(i));
-  EACH_UNIT(i) load_vec(a.w, UNIT(i), a.w_off, w[i]);
+  EACH_UNIT(i) w[i] = load_vec(a.w, UNIT(i), a.w_off);
   for (int64_t t = at.row; t < a.T; t += at.stride) {
-    float x[U][8], sum[1] = {0.0f};
+    Vec8 x[U];
+    f32x2 s = 0;
     EACH_UNIT(i) {
-      qx[i].get(x[i]);
+      x[i] = qx[i].get();
       if (t + at.stride < a.T) qx[i].load(a.x, (t + at.stride) * a.units + UNIT(i));
-      EACH(c) sum[0] = fmaf(x[i][c], x[i][c], sum[0]);
+      EACH(c) s = fma2(x[i].p[c], x[i].p[c], s);
     }
+    float sum[1] = {sum2(s)};
     group_sum(sum, slot);
     const float rstd = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rstd;
     EACH_UNIT(i) {
-      EACH(c) x[i][c] = x[i][c] * rstd * w[i][c];
+      EACH(c) x[i].p[c] = mul2(mul2(x[i].p[c], both(rstd)), w[i].p[c]);
       Unit8<uint16_t> q;
       q.set(x[i]);
       q.store(a.n, t * a.units + UNIT(i));
@@ -115,20 +122,27 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_before_kernel(NormAr
   }
 }
 
-// One gate value per element of unit u of row t.
-__device__ __forceinline__ void gate_of(const NormArgs& a, int64_t t, int u, const float (&gc)[8], float gt, float (&g)[8]) {
-  if (a.gate_kind == MOE_GATE_ELEMENT) {
-    Unit8<uint16_t> q;
-    q.load(a.gate, t * a.units + u);
-    q.get(g);
-  } else {
-    EACH(c) g[c] = a.gate_kind == MOE_GATE_CHANNEL ? gc[c] : gt;
+// The weights times the gate of a channel, and the gate of a token (1 where the gate is another).
+__device__ __forceinline__ Vec8 gated_weight(const NormArgs& a, int u) {
+  Vec8 w = load_vec(a.w, u, a.w_off);
+  if (a.gate_kind == MOE_GATE_CHANNEL) {
+    const Vec8 g = load_vec(static_cast<const float*>(a.gate), u, 0.0f);
+    EACH(c) w.p[c] = mul2(w.p[c], g.p[c]);
   }
+  return w;
+}
+__device__ __forceinline__ float token_gate(const NormArgs& a, int64_t t) {
+  return a.gate_kind == MOE_GATE_TOKEN ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
+}
+__device__ __forceinline__ Vec8 element_gate(const NormArgs& a, int64_t unit) {
+  Unit8<uint16_t> q;
+  q.load(a.gate, unit);
+  return q.get();
 }
 
 template <typename R, typename Y, int U, int kMaxThreads, int kPerSm, bool kNext>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_after_kernel(NormArgs a) {
-  float w[U][8], gc[U][8], wn[U][8];
+  Vec8 w[U], wn[U];                       // w' times a channel's gate
   Unit8<Y> qy[U];
   Unit8<R> qx[U];
   int slot = 0;
@@ -142,43 +156,48 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_after_kernel(NormArg
   pdl_wait();
   if (at.row < a.T) load_row(at.row);
   EACH_UNIT(i) {
-    load_vec(a.w, UNIT(i), a.w_off, w[i]);
-    if (kNext) load_vec(a.w_next, UNIT(i), a.w_off, wn[i]);
-    if (a.gate_kind == MOE_GATE_CHANNEL) load_vec(static_cast<const float*>(a.gate), UNIT(i), 0.0f, gc[i]);
+    w[i] = gated_weight(a, UNIT(i));
+    if (kNext) wn[i] = load_vec(a.w_next, UNIT(i), a.w_off);
   }
   for (int64_t t = at.row; t < a.T; t += at.stride) {
-    float y[U][8], sum[1] = {0.0f};
+    Vec8 y[U];
     Unit8<R> x[U];
+    f32x2 s = 0;
     EACH_UNIT(i) {
-      qy[i].get(y[i]);
+      y[i] = qy[i].get();
       x[i] = qx[i];
-      EACH(c) sum[0] = fmaf(y[i][c], y[i][c], sum[0]);
+      EACH(c) s = fma2(y[i].p[c], y[i].p[c], s);
     }
     if (t + at.stride < a.T) load_row(t + at.stride);
+    float sum[1] = {sum2(s)};
     group_sum(sum, slot);
     const float rstd = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rstd;
-    const float gt = a.gate_kind == MOE_GATE_TOKEN ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
-    sum[0] = 0.0f;
+    const f32x2 scale = both(a.b * token_gate(a, t) * rstd), ra = both(a.a);
+    s = 0;
     EACH_UNIT(i) {
-      float xv[8], g[8];
-      x[i].get(xv);
-      gate_of(a, t, UNIT(i), gc[i], gt, g);
-      EACH(c) y[i][c] = a.a * xv[c] + a.b * g[c] * (y[i][c] * rstd * w[i][c]);
+      const Vec8 xv = x[i].get();
+      EACH(c) y[i].p[c] = mul2(mul2(y[i].p[c], scale), w[i].p[c]);
+      if (a.gate_kind == MOE_GATE_ELEMENT) {
+        const Vec8 g = element_gate(a, t * a.units + UNIT(i));
+        EACH(c) y[i].p[c] = mul2(y[i].p[c], g.p[c]);
+      }
+      EACH(c) y[i].p[c] = fma2(xv.p[c], ra, y[i].p[c]);
       Unit8<R> q;
       q.set(y[i]);
       q.store(a.out, t * a.units + UNIT(i));
       if (kNext) {
-        q.get(y[i]);   // the stored stream, as a separate norm would read it
-        EACH(c) sum[0] = fmaf(y[i][c], y[i][c], sum[0]);
+        y[i] = q.get();   // the stored stream, as a separate norm would read it
+        EACH(c) s = fma2(y[i].p[c], y[i].p[c], s);
       }
     }
     if (kNext) {
+      sum[0] = sum2(s);
       group_sum(sum, slot);
       const float rn = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
       if (threadIdx.x == 0 && a.rstd_next) a.rstd_next[t] = rn;
       EACH_UNIT(i) {
-        EACH(c) y[i][c] = y[i][c] * rn * wn[i][c];
+        EACH(c) y[i].p[c] = mul2(mul2(y[i].p[c], both(rn)), wn[i].p[c]);
         Unit8<uint16_t> q;
         q.set(y[i]);
         q.store(a.n, t * a.units + UNIT(i));
@@ -189,22 +208,16 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_after_kernel(NormArg
 
 // Adds the groups' column sums in group order (through shared memory) and writes the CTA's row.
 template <int U>
-__device__ __forceinline__ void write_part(const NormArgs& a, int which, float (&s)[U][8], float* s_cols) {
-  float4* mine = reinterpret_cast<float4*>(s_cols) + ((threadIdx.y - 1) * blockDim.x + threadIdx.x) * 2;
+__device__ __forceinline__ void write_part(const NormArgs& a, int which, Vec8 (&s)[U], Vec8* s_cols) {
   if (blockDim.y > 1) {                 // one unit per thread then
     __syncthreads();
-    if (threadIdx.y > 0) {
-      mine[0] = make_float4(s[0][0], s[0][1], s[0][2], s[0][3]);
-      mine[1] = make_float4(s[0][4], s[0][5], s[0][6], s[0][7]);
-    }
+    if (threadIdx.y > 0) s_cols[(threadIdx.y - 1) * blockDim.x + threadIdx.x] = s[0];
     __syncthreads();
   }
   if (threadIdx.y > 0) return;
   for (int g = 1; g < static_cast<int>(blockDim.y); ++g) {
-    const float4* q = reinterpret_cast<const float4*>(s_cols) + ((g - 1) * blockDim.x + threadIdx.x) * 2;
-    const float4 lo = q[0], hi = q[1];
-    s[0][0] += lo.x; s[0][1] += lo.y; s[0][2] += lo.z; s[0][3] += lo.w;
-    s[0][4] += hi.x; s[0][5] += hi.y; s[0][6] += hi.z; s[0][7] += hi.w;
+    const Vec8 o = s_cols[(g - 1) * blockDim.x + threadIdx.x];
+    EACH(c) s[0].p[c] = add2(s[0].p[c], o.p[c]);
   }
   float* row = a.part + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.units * 8;
   EACH_UNIT(i) {
@@ -218,8 +231,8 @@ constexpr int kGradThreads = 512;       // threads of a gradient's CTA, groups o
 
 template <typename R, int U, int kMaxThreads>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_before_grad_kernel(NormArgs a) {
-  __shared__ __align__(16) float s_cols[kGradThreads * 8];
-  float w[U][8], dw[U][8];
+  __shared__ Vec8 s_cols[kGradThreads];
+  Vec8 w[U], dw[U];
   Unit8<R> qx[U], qr[U];
   Unit8<uint16_t> qd[U];
   float q_rstd = 0.0f;
@@ -236,32 +249,34 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_before_grad_kernel(NormAr
   pdl_wait();
   if (at.row < a.T) load_row(at.row);
   EACH_UNIT(i) {
-    load_vec(a.w, UNIT(i), a.w_off, w[i]);
-    EACH(c) dw[i][c] = 0.0f;
+    w[i] = load_vec(a.w, UNIT(i), a.w_off);
+    EACH(c) dw[i].p[c] = 0;
   }
   for (int64_t t = at.row; t < a.T; t += at.stride) {
     const float rstd = q_rstd;
-    float xh[U][8], d[U][8], dot[1] = {0.0f};
+    Vec8 xh[U], d[U];
     Unit8<R> res[U];
+    f32x2 s = 0;
     EACH_UNIT(i) {
-      qx[i].get(xh[i]);
-      qd[i].get(d[i]);
+      xh[i] = qx[i].get();
+      d[i] = qd[i].get();
       res[i] = qr[i];
       EACH(c) {
-        xh[i][c] *= rstd;
-        dw[i][c] = fmaf(d[i][c], xh[i][c], dw[i][c]);
-        d[i][c] *= w[i][c];
-        dot[0] = fmaf(d[i][c], xh[i][c], dot[0]);
+        xh[i].p[c] = mul2(xh[i].p[c], both(rstd));
+        dw[i].p[c] = fma2(d[i].p[c], xh[i].p[c], dw[i].p[c]);
+        d[i].p[c] = mul2(d[i].p[c], w[i].p[c]);
+        s = fma2(d[i].p[c], xh[i].p[c], s);
       }
     }
     if (t + at.stride < a.T) load_row(t + at.stride);
+    float dot[1] = {sum2(s)};
     group_sum(dot, slot);
-    const float m = dot[0] * a.inv_h;
+    const f32x2 m = both(-dot[0] * a.inv_h);
     EACH_UNIT(i) {
-      float r[8];
-      if (a.dres) res[i].get(r);
-      else EACH(c) r[c] = 0.0f;
-      EACH(c) r[c] += rstd * (d[i][c] - xh[i][c] * m);
+      Vec8 r;
+      if (a.dres) r = res[i].get();
+      else EACH(c) r.p[c] = 0;
+      EACH(c) r.p[c] = fma2(both(rstd), fma2(xh[i].p[c], m, d[i].p[c]), r.p[c]);
       Unit8<R> q;
       q.set(r);
       q.store(a.dx, t * a.units + UNIT(i));
@@ -270,12 +285,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_before_grad_kernel(NormAr
   write_part<U>(a, 0, dw, s_cols);
 }
 
-// Gradient of `after`: with d = dout (+ the gradient that comes through the next norm, whose input
-// is the stored out),  dx = a d,  dgate = b d rms(y) w',  and the norm's gradient of b d g.
+// Gradient of `after`.  With oh, yh the normed rows of the stored out and of y, e = dn w_next',
+// u = dout + rn e and v = b g w' yh (g here without a token's gate gt):
+//   d  = dout + (the gradient through the next norm) = u - rn mean(e oh) oh,       dx = a d
+//   dy = rstd (gt b g w' d - gt mean(d v) yh),   sum(d v) = sum(u v) - rn mean(e oh) sum(oh v),
+// so the three row sums e oh, u v and oh v are taken together.  A token's gate has the gradient
+// sum(d v); an element's b w' d yh.  The column sum q = sum_t d yh (times a token's or an
+// element's gate) is the branch weight's gradient over b g, and a channel gate's over b w'.
 template <typename R, typename Y, int U, int kMaxThreads, bool kNext>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArgs a) {
-  __shared__ __align__(16) float s_cols[kGradThreads * 8];
-  float dw[U][8], dwn[U][8], dg[U][8];
+  __shared__ Vec8 s_cols[kGradThreads];
+  Vec8 q_col[U], dwn[U], bw[U], wn[U];    // bw: b w' times a channel's gate
   Unit8<R> qd[U], qo[U];
   Unit8<Y> qy[U];
   Unit8<uint16_t> qn[U];
@@ -298,109 +318,134 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArg
   pdl_wait();
   if (at.row < a.T) load_row(at.row);
   EACH_UNIT(i) {
+    bw[i] = gated_weight(a, UNIT(i));
+    if (kNext) wn[i] = load_vec(a.w_next, UNIT(i), a.w_off);
     EACH(c) {
-      dw[i][c] = 0.0f;
-      dwn[i][c] = 0.0f;
-      dg[i][c] = 0.0f;
+      bw[i].p[c] = mul2(bw[i].p[c], both(a.b));
+      q_col[i].p[c] = 0;
+      dwn[i].p[c] = 0;
     }
   }
+  const bool by_element = a.gate_kind == MOE_GATE_ELEMENT;
   for (int64_t t = at.row; t < a.T; t += at.stride) {
     const float rstd = q_rstd, rn = q_rn;
-    float d[U][8], yh[U][8], oh[U][8], e[U][8], dot[1] = {0.0f};
+    Vec8 d[U], yh[U], oh[U];
+    f32x2 s_eo = 0, s_uv = 0, s_ov = 0;
     EACH_UNIT(i) {
-      qd[i].get(d[i]);
-      qy[i].get(yh[i]);
+      d[i] = qd[i].get();
+      yh[i] = qy[i].get();
+      EACH(c) yh[i].p[c] = mul2(yh[i].p[c], both(rstd));
+      Vec8 v;
+      EACH(c) v.p[c] = mul2(yh[i].p[c], bw[i].p[c]);
+      if (by_element) {
+        const Vec8 g = element_gate(a, t * a.units + UNIT(i));
+        EACH(c) v.p[c] = mul2(v.p[c], g.p[c]);
+      }
       if (kNext) {
-        float wn[8];
-        load_vec(a.w_next, UNIT(i), a.w_off, wn);
-        qo[i].get(oh[i]);
-        qn[i].get(e[i]);
+        oh[i] = qo[i].get();
+        Vec8 e = qn[i].get();
         EACH(c) {
-          oh[i][c] *= rn;
-          dwn[i][c] = fmaf(e[i][c], oh[i][c], dwn[i][c]);
-          e[i][c] *= wn[c];
-          dot[0] = fmaf(e[i][c], oh[i][c], dot[0]);
+          oh[i].p[c] = mul2(oh[i].p[c], both(rn));
+          dwn[i].p[c] = fma2(e.p[c], oh[i].p[c], dwn[i].p[c]);
+          e.p[c] = mul2(e.p[c], wn[i].p[c]);
+          d[i].p[c] = fma2(e.p[c], both(rn), d[i].p[c]);
+          s_eo = fma2(e.p[c], oh[i].p[c], s_eo);
+          s_ov = fma2(oh[i].p[c], v.p[c], s_ov);
         }
       }
+      EACH(c) s_uv = fma2(d[i].p[c], v.p[c], s_uv);
     }
     if (t + at.stride < a.T) load_row(t + at.stride);
+    float dv, back = 0.0f;
     if (kNext) {
-      group_sum(dot, slot);
-      const float m = dot[0] * a.inv_h;
-      EACH_UNIT(i) EACH(c) d[i][c] += rn * (e[i][c] - oh[i][c] * m);
+      float sums[3] = {sum2(s_eo), sum2(s_uv), sum2(s_ov)};
+      group_sum(sums, slot);
+      back = -rn * (sums[0] * a.inv_h);
+      dv = fmaf(back, sums[2], sums[1]);
+    } else {
+      float sums[1] = {sum2(s_uv)};
+      group_sum(sums, slot);
+      dv = sums[0];
     }
-    const float gt = a.gate_kind == MOE_GATE_TOKEN ? __ldg(static_cast<const float*>(a.gate) + t) : 1.0f;
-    float sums[2] = {0.0f, 0.0f};
+    const float gt = token_gate(a, t);
+    if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(a.dgate)[t] = dv;
+    const f32x2 m = both(-rstd * gt * (dv * a.inv_h)), rg = both(rstd * gt);
     EACH_UNIT(i) {
-      float r[8], g[8], w[8];
-      EACH(c) r[c] = a.a * d[i][c];
+      const int64_t u = t * a.units + UNIT(i);
+      if (kNext) EACH(c) d[i].p[c] = fma2(oh[i].p[c], both(back), d[i].p[c]);
+      Vec8 r;
+      EACH(c) r.p[c] = mul2(d[i].p[c], both(a.a));
       Unit8<R> q;
       q.set(r);
-      q.store(a.dx, t * a.units + UNIT(i));
-      load_vec(a.w, UNIT(i), a.w_off, w);
-      float gc[8];
-      if (a.gate_kind == MOE_GATE_CHANNEL) load_vec(static_cast<const float*>(a.gate), UNIT(i), 0.0f, gc);
-      gate_of(a, t, UNIT(i), gc, gt, g);
-      EACH(c) {
-        yh[i][c] *= rstd;
-        d[i][c] *= a.b;
-        r[c] = d[i][c] * (yh[i][c] * w[c]);   // the gate's gradient
-        sums[1] += r[c];
-        dg[i][c] += r[c];
-        d[i][c] *= g[c];
-        dw[i][c] = fmaf(d[i][c], yh[i][c], dw[i][c]);
-        d[i][c] *= w[c];
-        sums[0] = fmaf(d[i][c], yh[i][c], sums[0]);
-      }
-      if (a.gate_kind == MOE_GATE_ELEMENT) {
+      q.store(a.dx, u);
+      if (by_element) {
+        const Vec8 g = element_gate(a, u);
+        EACH(c) {
+          r.p[c] = mul2(d[i].p[c], mul2(yh[i].p[c], bw[i].p[c]));
+          d[i].p[c] = mul2(d[i].p[c], g.p[c]);
+        }
         Unit8<uint16_t> qg;
         qg.set(r);
-        qg.store(a.dgate, t * a.units + UNIT(i));
+        qg.store(a.dgate, u);
       }
-    }
-    group_sum(sums, slot);
-    if (a.gate_kind == MOE_GATE_TOKEN && threadIdx.x == 0) static_cast<float*>(a.dgate)[t] = sums[1];
-    const float m = sums[0] * a.inv_h;
-    EACH_UNIT(i) {
-      EACH(c) d[i][c] = rstd * (d[i][c] - yh[i][c] * m);
-      Unit8<Y> q;
-      q.set(d[i]);
-      q.store(a.dy, t * a.units + UNIT(i));
+      EACH(c) {
+        q_col[i].p[c] = fma2(mul2(d[i].p[c], both(gt)), yh[i].p[c], q_col[i].p[c]);
+        d[i].p[c] = fma2(yh[i].p[c], m, mul2(mul2(d[i].p[c], bw[i].p[c]), rg));
+      }
+      Unit8<Y> qq;
+      qq.set(d[i]);
+      qq.store(a.dy, u);
     }
   }
-  write_part<U>(a, 0, dw, s_cols);
+  write_part<U>(a, 0, q_col, s_cols);
   if (kNext) write_part<U>(a, 1, dwn, s_cols);
-  if (a.gate_kind == MOE_GATE_CHANNEL) write_part<U>(a, 2, dg, s_cols);
 }
 
-// Column sums: part [3][rows][H] -> one vector each (NULL: skipped).  32 columns per CTA, 32
-// threads per column, each over every 32nd row; then one sum over the 32 in a fixed order.
-__global__ void __launch_bounds__(1024) norm_columns_kernel(const float* __restrict__ part, int rows, int H, float* o0,
-                                                            float* o1, float* o2) {
-  __shared__ float s_sum[32][33];
-  float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
+// Column sums of part [2][rows][H], 32 columns per CTA: eight threads of four columns, 32 runs of
+// rows, then the runs in order.  The first becomes dw = b g q (g: a channel gate or NULL: 1) and,
+// with a channel gate, dgate = b w' q; the second dw_next.
+__global__ void __launch_bounds__(256) norm_columns_kernel(const float* __restrict__ part, int rows, int H, float b,
+                                                           const float* __restrict__ gate, const float* __restrict__ w,
+                                                           float w_off, float* dw, float* dgate, float* dw_next) {
+  __shared__ float4 s_sum[32][8];
+  const int c = threadIdx.x & 7, r = threadIdx.x >> 3;
+  const int col = blockIdx.x * 32 + c * 4;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   pdl_wait();
-  if (!out) return;
-  const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + c;
-  float v = 0.0f;
-  if (col < H)
-    for (int i = r; i < rows; i += 32) v += part[(static_cast<int64_t>(blockIdx.y) * rows + i) * H + col];
-  s_sum[c][r] = v;
+  if (col < H) {
+    const float* p = part + static_cast<int64_t>(blockIdx.y) * rows * H + col;
+#pragma unroll 5
+    for (int i = r; i < rows; i += 32) {
+      const float4 q = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(i) * H);
+      v.x += q.x; v.y += q.y; v.z += q.z; v.w += q.w;
+    }
+  }
+  s_sum[r][c] = v;
   __syncthreads();
-  v = s_sum[r][c];
+  const int mine = blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x >= 32 || mine >= H) return;
+  float t = 0.0f;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if (c == 0 && blockIdx.x * 32 + r < H) out[blockIdx.x * 32 + r] = v;
+  for (int i = 0; i < 32; ++i) t += reinterpret_cast<const float*>(&s_sum[i][0])[threadIdx.x];
+  if (blockIdx.y == 1) {
+    dw_next[mine] = t;
+  } else {
+    dw[mine] = t * (gate ? b * __ldg(gate + mine) : b);
+    if (dgate) dgate[mine] = t * (b * (__ldg(w + mine) + w_off));
+  }
 }
 
-constexpr int kOneUnit = 512;    // rows of up to this many units: one unit per thread, else two
+// Units per thread: gradients one for rows of up to kOneUnit units, else two; forward one up to 32
+// units, else two: a row's sums cost a thread about as many instructions as a unit's arithmetic, and
+// the forward kernels are bound by their instructions (32768 x 2048 with the next norm: 115 us with
+// one and 87 us with two).
+constexpr int kOneUnit = 512;
 constexpr int kForwardThreads = 256;
 constexpr int kMaxSms = 160;     // the workspace holds the column sums of this many CTAs
 
 // Threads of a row: 32, 64 or a multiple of 128.
-int row_threads(int units) {
-  const int per = units <= kOneUnit ? units : (units + 1) / 2;
+int row_threads(int units, int one_unit) {
+  const int per = units <= one_unit ? units : (units + 1) / 2;
   return per <= 32 ? 32 : per <= 64 ? 64 : (per + 127) / 128 * 128;
 }
 
@@ -408,17 +453,17 @@ int row_threads(int units) {
 struct NormLaunch {
   dim3 grid, block;
 };
-NormLaunch launch_of(int64_t T, int units, int threads, int per_sm, int n_sm) {
-  const int x = row_threads(units), y = std::max(1, threads / x);
+NormLaunch launch_of(int64_t T, int units, int one_unit, int threads, int per_sm, int n_sm) {
+  const int x = row_threads(units, one_unit), y = std::max(1, threads / x);
   const int64_t most = static_cast<int64_t>(n_sm) * std::max(1, per_sm * threads / (x * y));
   NormLaunch l;
   l.block = dim3(x, y);
   l.grid = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min((T + y - 1) / y, most))));
   return l;
 }
-NormLaunch forward_launch(int64_t T, int units, int n_sm) { return launch_of(T, units, kForwardThreads, 4, n_sm); }
+NormLaunch forward_launch(int64_t T, int units, int n_sm) { return launch_of(T, units, 32, kForwardThreads, 2, n_sm); }
 NormLaunch grad_launch(int64_t T, int units, int n_sm) {
-  return launch_of(T, units, kGradThreads, 1, std::min(n_sm, kMaxSms));
+  return launch_of(T, units, kOneUnit, kGradThreads, 1, std::min(n_sm, kMaxSms));
 }
 
 NormArgs args_of(const moe_norm_t& s) {
@@ -434,16 +479,15 @@ NormArgs args_of(const moe_norm_t& s) {
   return a;
 }
 
-// Launch bounds: up to 256 threads four CTAs per SM (64 registers), else one CTA; two units per
-// thread in up to 512 threads (128 registers), and in 1024 (64, some spilled) above 8192 columns.
-#define PICK_UNITS(small, one, two, more) \
-  (s.H / 8 <= 256 ? small : s.H / 8 <= kOneUnit ? one : s.H / 8 <= 2 * kOneUnit ? two : more)
-#define PICK_BEFORE(K, R) PICK_UNITS((K<R, 1, 256, 4>), (K<R, 1, 512, 1>), (K<R, 2, 512, 1>), (K<R, 2, 1024, 1>))
-#define PICK_GRAD(K, R) PICK_UNITS((K<R, 1, 512>), (K<R, 1, 512>), (K<R, 2, 512>), (K<R, 2, 1024>))
+// Launch bounds of 256 or 512 threads leave 128 registers, those of 1024 (above 8192 columns) 64,
+// some of them spilled.
+#define PICK_FORWARD(one, two, wide, more) (s.H / 8 <= 32 ? one : s.H / 8 <= 512 ? two : s.H / 8 <= 1024 ? wide : more)
+#define PICK_GRADIENT(one, two, more) (s.H / 8 <= kOneUnit ? one : s.H / 8 <= 2 * kOneUnit ? two : more)
+#define PICK_BEFORE(K, R) PICK_FORWARD((K<R, 1, 256, 2>), (K<R, 2, 256, 2>), (K<R, 2, 512, 1>), (K<R, 2, 1024, 1>))
+#define PICK_GRAD(K, R) PICK_GRADIENT((K<R, 1, 512>), (K<R, 2, 512>), (K<R, 2, 1024>))
 #define PICK_AFTER(K, R, Y, next) \
-  PICK_UNITS((K<R, Y, 1, 256, 4, next>), (K<R, Y, 1, 512, 1, next>), (K<R, Y, 2, 512, 1, next>), (K<R, Y, 2, 1024, 1, next>))
-#define PICK_AFTER_GRAD(K, R, Y, next) \
-  PICK_UNITS((K<R, Y, 1, 512, next>), (K<R, Y, 1, 512, next>), (K<R, Y, 2, 512, next>), (K<R, Y, 2, 1024, next>))
+  PICK_FORWARD((K<R, Y, 1, 256, 2, next>), (K<R, Y, 2, 256, 2, next>), (K<R, Y, 2, 512, 1, next>), (K<R, Y, 2, 1024, 1, next>))
+#define PICK_AFTER_GRAD(K, R, Y, next) PICK_GRADIENT((K<R, Y, 1, 512, next>), (K<R, Y, 2, 512, next>), (K<R, Y, 2, 1024, next>))
 #define PICK_NEXT(PICK, K, R, Y) (next ? PICK(K, R, Y, true) : PICK(K, R, Y, false))
 #define PICK_TYPES(PICK, K)                                                                                          \
   (s.residual_fp32 ? (s.branch_fp32 ? PICK_NEXT(PICK, K, float, float) : PICK_NEXT(PICK, K, float, uint16_t))        \
@@ -507,9 +551,9 @@ cudaError_t launch_norm_before_grad(const moe_norm_t& s, const void* dn, const v
   auto kern = s.residual_fp32 ? PICK_GRAD(norm_before_grad_kernel, float) : PICK_GRAD(norm_before_grad_kernel, uint16_t);
   e = launch_pdl(true, kern, l.grid, l.block, 0, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(true, norm_columns_kernel, dim3((s.H + 31) / 32, 1), dim3(1024), 0, st,
-                    static_cast<const float*>(part), grid, s.H, dw, static_cast<float*>(nullptr),
-                    static_cast<float*>(nullptr));
+  return launch_pdl(true, norm_columns_kernel, dim3((s.H + 31) / 32, 1), dim3(256), 0, st,
+                    static_cast<const float*>(part), grid, s.H, 1.0f, static_cast<const float*>(nullptr), w,
+                    s.weight_offset, dw, static_cast<float*>(nullptr), static_cast<float*>(nullptr));
 }
 
 cudaError_t launch_norm_after_grad(const moe_norm_t& s, const void* dout, const void* dn, const void* y, const void* out,
@@ -539,9 +583,11 @@ cudaError_t launch_norm_after_grad(const moe_norm_t& s, const void* dout, const 
   auto kern = PICK_TYPES(PICK_AFTER_GRAD, norm_after_grad_kernel);
   e = launch_pdl(true, kern, l.grid, l.block, 0, st, a);
   if (e != cudaSuccess) return e;
-  float* dgc = s.gate == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
-  return launch_pdl(true, norm_columns_kernel, dim3((s.H + 31) / 32, dgc ? 3 : dw_next ? 2 : 1), dim3(1024), 0, st,
-                    static_cast<const float*>(part), grid, s.H, dw, dw_next, dgc);
+  const bool channel = s.gate == MOE_GATE_CHANNEL;
+  return launch_pdl(true, norm_columns_kernel, dim3((s.H + 31) / 32, next ? 2 : 1), dim3(256), 0, st,
+                    static_cast<const float*>(part), grid, s.H, s.branch_scale,
+                    channel ? static_cast<const float*>(gate) : nullptr, w, s.weight_offset, dw,
+                    channel ? static_cast<float*>(dgate) : nullptr, dw_next);
 }
 
 }  // namespace moe

@@ -1,10 +1,49 @@
-// Units of eight consecutive row elements (bf16: 16 bytes, fp32: 32 bytes) as fp32 values.
+// Units of eight consecutive row elements (bf16: 16 bytes, fp32: 32 bytes), computed with as four
+// packed pairs of fp32 values (one instruction per pair).
 #pragma once
 
 #include "internal.cuh"
 
 namespace moe {
 
+typedef uint64_t f32x2;
+
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f32x2 both(float v) { return pack2(v, v); }
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(f32x2 v) {
+  const float2 f = unpack2(v);
+  return f.x + f.y;
+}
+
+struct Vec8 {
+  f32x2 p[4];
+};
+
+// Eight elements of a row as they lie in memory.
 template <typename V>
 struct Unit8;
 
@@ -12,19 +51,19 @@ template <>
 struct Unit8<uint16_t> {
   uint4 q;
   __device__ __forceinline__ void load(const void* base, int64_t unit) { q = __ldg(static_cast<const uint4*>(base) + unit); }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ Vec8 get() const {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    Vec8 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) v.p[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    return v;
   }
-  __device__ __forceinline__ void set(const float (&f)[8]) {
+  __device__ __forceinline__ void set(const Vec8& v) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      const float2 f = unpack2(v.p[i]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     q = make_uint4(w[0], w[1], w[2], w[3]);
@@ -39,13 +78,18 @@ struct Unit8<float> {
     a = __ldg(static_cast<const float4*>(base) + 2 * unit);
     b = __ldg(static_cast<const float4*>(base) + 2 * unit + 1);
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  __device__ __forceinline__ Vec8 get() const {
+    Vec8 v;
+    v.p[0] = pack2(a.x, a.y);
+    v.p[1] = pack2(a.z, a.w);
+    v.p[2] = pack2(b.x, b.y);
+    v.p[3] = pack2(b.z, b.w);
+    return v;
   }
-  __device__ __forceinline__ void set(const float (&f)[8]) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ __forceinline__ void set(const Vec8& v) {
+    const float2 p = unpack2(v.p[0]), q = unpack2(v.p[1]), r = unpack2(v.p[2]), s = unpack2(v.p[3]);
+    a = make_float4(p.x, p.y, q.x, q.y);
+    b = make_float4(r.x, r.y, s.x, s.y);
   }
   __device__ __forceinline__ void store(void* base, int64_t unit) const {
     static_cast<float4*>(base)[2 * unit] = a;
