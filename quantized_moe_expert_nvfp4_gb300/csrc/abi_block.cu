@@ -31,15 +31,8 @@ moe_status_t check_tokens(const moe_tokens_t* s) {
 
 SortShape sort_shape(const moe_tokens_t& s) { return {s.T, s.H, s.E, s.k, s.fp32 != 0}; }
 
-struct SortWs {
-  size_t hist, totals, total;
-};
-SortWs sort_ws(int64_t S, int E) {
-  SortWs w;
-  w.hist = kStatusBytes;
-  w.totals = align256(w.hist + sizeof(int32_t) * static_cast<size_t>(sort_chunks(S)) * (E + 1));
-  w.total = align256(w.totals + sizeof(int32_t) * static_cast<size_t>(E + 1));
-  return w;
+size_t sort_ws_bytes(int64_t S, int E) {   // the status word, then hist [chunks, E + 1]
+  return align256(kStatusBytes + sizeof(int32_t) * static_cast<size_t>(sort_chunks(S)) * (E + 1));
 }
 
 moe_status_t check_block_weights(const moe_block_fp8_weights_t* w) {
@@ -85,7 +78,7 @@ extern "C" {
 size_t moe_sort_workspace_size(int32_t T, int32_t E, int32_t k) {
   const moe_tokens_t s = {T, 8, E, k, 0};
   if (check_tokens(&s) != MOE_OK) return 0;
-  return sort_ws(static_cast<int64_t>(T) * k, E).total;
+  return sort_ws_bytes(static_cast<int64_t>(T) * k, E);
 }
 
 moe_status_t moe_sort_tokens(const void* x, const int32_t* topk_ids, const moe_tokens_t* shape, void* xs, int32_t* offsets,
@@ -95,15 +88,14 @@ moe_status_t moe_sort_tokens(const void* x, const int32_t* topk_ids, const moe_t
   if (!aligned16(offsets)) return MOE_ERR_INVALID_ARG;
   if (shape->T > 0 && (!aligned16(x) || !aligned16(topk_ids) || !aligned16(xs) || !aligned16(sorted_slot) || !aligned16(slot_pos)))
     return MOE_ERR_INVALID_ARG;
-  const SortWs L = sort_ws(static_cast<int64_t>(shape->T) * shape->k, shape->E);
-  if ((st = check_ws_bytes(ws, ws_bytes, L.total)) != MOE_OK) return st;
+  if ((st = check_ws_bytes(ws, ws_bytes, sort_ws_bytes(static_cast<int64_t>(shape->T) * shape->k, shape->E))) != MOE_OK)
+    return st;
   if ((st = check_device(stream)) != MOE_OK) return st;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (shape->T == 0) return cuda_status(cudaMemsetAsync(offsets, 0, sizeof(int32_t) * (shape->E + 1), cs));
   char* b = static_cast<char*>(ws);
   return cuda_status(launch_sort_tokens(sort_shape(*shape), x, topk_ids, xs, offsets, sorted_slot, slot_pos,
-                                        reinterpret_cast<int32_t*>(b + L.hist), reinterpret_cast<int32_t*>(b + L.totals),
-                                        reinterpret_cast<int32_t*>(b), cs));
+                                        reinterpret_cast<int32_t*>(b + kStatusBytes), reinterpret_cast<int32_t*>(b), cs));
 }
 
 moe_status_t moe_sort_tokens_backward(const void* dxs, const int32_t* slot_pos, const moe_tokens_t* shape, void* dx,

@@ -336,8 +336,7 @@ struct SortShape {
 };
 int64_t sort_chunks(int64_t S);   // rows of hist [chunks, E + 1]
 cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t* ids, void* xs, int32_t* offsets,
-                               int32_t* sorted_slot, int32_t* slot_pos, int32_t* hist, int32_t* totals, int32_t* status,
-                               cudaStream_t st);
+                               int32_t* sorted_slot, int32_t* slot_pos, int32_t* hist, int32_t* status, cudaStream_t st);
 // w NULL: weights 1; shared NULL: none.
 cudaError_t launch_return_tokens(const SortShape& s, const void* rows, const int32_t* slot_pos, const float* w,
                                  const void* shared, void* out, cudaStream_t st);

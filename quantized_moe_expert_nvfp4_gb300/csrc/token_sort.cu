@@ -19,8 +19,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 1024;                 // slots per CTA of the counting and placing kernels
-constexpr int kPerWarp = kChunk / kWarps;
+constexpr int kMaxChunks = 64;               // CTAs of the counting sort, a run of slots each
+constexpr int kMinChunk = 1024;
+constexpr int kSortThreads = 1024;
+constexpr int kPlaceWarps = 16;              // warps that place a chunk's slots
 
 __device__ __forceinline__ int key_of(int id, int E) { return static_cast<unsigned>(id) < static_cast<unsigned>(E) ? id : E; }
 
@@ -74,95 +76,70 @@ __global__ void __launch_bounds__(kThreads) sort_rank_kernel(const uint4* __rest
 }
 
 // ------------------------------------------------------------------ counting sort (any batch)
+// Three launches: the keys' counts of each chunk of slots; the placement, in which every CTA adds up
+// the counts of the chunks before its own; and the copies of the rows.  Each launch starts while the
+// one before it drains, and x, older than all of them, is read before the wait for the placement.
+
 // hist[c][key]: slots of chunk c with that key.
-__global__ void __launch_bounds__(kThreads) sort_count_kernel(const int32_t* __restrict__ ids, int S, int E,
-                                                              int32_t* __restrict__ hist, int32_t* status) {
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const int32_t* __restrict__ ids, int S, int chunk, int E,
+                                                                  int32_t* __restrict__ hist, int32_t* status) {
   __shared__ int s_cnt[kMaxE + 1];
   pdl_wait_then_release();
-  for (int e = threadIdx.x; e <= E; e += kThreads) s_cnt[e] = 0;
+  for (int e = threadIdx.x; e <= E; e += kSortThreads) s_cnt[e] = 0;
   __syncthreads();
-  const int64_t s0 = static_cast<int64_t>(blockIdx.x) * kChunk;
-#pragma unroll
-  for (int i = 0; i < kChunk / kThreads; ++i) {
-    const int64_t s = s0 + i * kThreads + threadIdx.x;
-    if (s < S) {
-      const int id = __ldg(ids + s);
-      if (id >= E) report_device_error(status, kDevBadIndex);
-      atomicAdd(&s_cnt[key_of(id, E)], 1);
-    }
+  const int64_t s0 = static_cast<int64_t>(blockIdx.x) * chunk;
+  const int64_t s1 = min(s0 + chunk, static_cast<int64_t>(S));
+#pragma unroll 4
+  for (int64_t s = s0 + threadIdx.x; s < s1; s += kSortThreads) {
+    const int id = __ldg(ids + s);
+    if (id >= E) report_device_error(status, kDevBadIndex);
+    atomicAdd(&s_cnt[key_of(id, E)], 1);
   }
   __syncthreads();
   int32_t* h = hist + static_cast<int64_t>(blockIdx.x) * (E + 1);
-  for (int e = threadIdx.x; e <= E; e += kThreads) h[e] = s_cnt[e];
+  for (int e = threadIdx.x; e <= E; e += kSortThreads) h[e] = s_cnt[e];
 }
 
-// Column-wise exclusive prefix of hist over the chunks, in place, and the columns' totals: 32 keys
-// per CTA, 32 threads per key, each over a contiguous run of chunks.
-__global__ void __launch_bounds__(1024) sort_scan_kernel(int32_t* __restrict__ hist, int chunks, int E,
-                                                         int32_t* __restrict__ totals) {
-  __shared__ int s_sum[32][33];
-  pdl_wait_then_release();
-  const int c = threadIdx.x & 31, seg = threadIdx.x >> 5;
-  const int e = blockIdx.x * 32 + c;
-  const int per = (chunks + 31) / 32;
-  const int a = min(chunks, seg * per), b = min(chunks, a + per);
-  int sum = 0;
-  if (e <= E)
-    for (int i = a; i < b; ++i) sum += hist[static_cast<int64_t>(i) * (E + 1) + e];
-  s_sum[c][seg] = sum;
-  __syncthreads();
-  {   // warp `seg` scans key `seg` of the CTA over the 32 runs
-    const int v = s_sum[seg][c];
-    int incl = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (c >= d) incl += o;
-    }
-    s_sum[seg][c] = incl - v;
-    if (c == 31 && blockIdx.x * 32 + seg <= E) totals[blockIdx.x * 32 + seg] = incl;
-  }
-  __syncthreads();
-  if (e <= E) {
-    int run = s_sum[c][seg];
-    for (int i = a; i < b; ++i) {
-      int32_t* h = hist + static_cast<int64_t>(i) * (E + 1) + e;
-      const int v = *h;
-      *h = run;
-      run += v;
-    }
-  }
-}
-
-// Places one chunk's slots: every warp counts its run of the chunk, each key's cursor is split
-// into per-warp cursors in run order, and each warp places its run 32 slots at a time (equal keys
-// of a group in lane order).
-__global__ void __launch_bounds__(kThreads) sort_place_kernel(const int32_t* __restrict__ ids, int S, int E,
-                                                              const int32_t* __restrict__ hist,
-                                                              const int32_t* __restrict__ totals,
-                                                              int32_t* __restrict__ offsets,
-                                                              int32_t* __restrict__ sorted_slot,
-                                                              int32_t* __restrict__ slot_pos) {
-  extern __shared__ int s_cur[];               // [kWarps][E + 1]
-  __shared__ int s_wsum[kWarps];
+// Places one chunk's slots: kPlaceWarps warps count a run of the chunk each, each key's cursor is
+// split into per-warp cursors in run order, and each warp places its run 32 slots at a time (equal
+// keys of a group in lane order).
+__global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t* __restrict__ ids, int S, int chunk, int E,
+                                                                  const int32_t* __restrict__ hist,
+                                                                  int32_t* __restrict__ offsets,
+                                                                  int32_t* __restrict__ sorted_slot,
+                                                                  int32_t* __restrict__ slot_pos) {
+  extern __shared__ int s_cur[];               // [kPlaceWarps][E + 1], then total and before [E + 1]
+  __shared__ int s_wsum[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = E + 1;
-  for (int i = threadIdx.x; i < kWarps * n; i += kThreads) s_cur[i] = 0;
-  pdl_wait();
+  int* s_total = s_cur + kPlaceWarps * n;
+  int* s_before = s_total + n;
+  const int c0 = blockIdx.x * chunk, slots = min(chunk, S - c0);
+  for (int i = threadIdx.x; i < kPlaceWarps * n; i += kSortThreads) s_cur[i] = 0;
   __syncthreads();
-  const int64_t w0 = static_cast<int64_t>(blockIdx.x) * kChunk + warp * kPerWarp;
-  int key[kPerWarp / 32];
-#pragma unroll
-  for (int i = 0; i < kPerWarp / 32; ++i) {
-    const int64_t s = w0 + i * 32 + lane;
-    key[i] = s < S ? key_of(__ldg(ids + s), E) : -1;
-    if (key[i] >= 0) atomicAdd(&s_cur[warp * n + key[i]], 1);
+  const int run_len = ((slots + kPlaceWarps - 1) / kPlaceWarps + 31) & ~31;
+  const int w0 = min(slots, warp * run_len), w1 = warp < kPlaceWarps ? min(slots, w0 + run_len) : w0;
+  // ids are older than the counting launch, hist is its result
+  for (int i = w0 + lane; i < w1; i += 32) atomicAdd(&s_cur[warp * n + key_of(__ldg(ids + c0 + i), E)], 1);
+  pdl_wait_then_release();
+  for (int e = threadIdx.x; e < n; e += kSortThreads) {
+    int total = 0, before = 0;
+    const int chunks = gridDim.x, mine = blockIdx.x;
+#pragma unroll 16
+    for (int c = 0; c < chunks; ++c) {
+      const int v = __ldg(hist + static_cast<int64_t>(c) * n + e);
+      total += v;
+      before += c < mine ? v : 0;
+    }
+    s_total[e] = total;
+    s_before[e] = before;
   }
+  __syncthreads();
   // exclusive prefix of the totals: a run of keys per thread
-  const int per = (n + kThreads - 1) / kThreads;
-  const int e0 = threadIdx.x * per, e1 = min(n, e0 + per);
+  const int per = (n + kSortThreads - 1) / kSortThreads;
+  const int e0 = min(n, static_cast<int>(threadIdx.x) * per), e1 = min(n, e0 + per);
   int sum = 0;
-  for (int e = e0; e < e1; ++e) sum += __ldg(totals + e);
+  for (int e = e0; e < e1; ++e) sum += s_total[e];
   int incl = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -173,48 +150,51 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(const int32_t* __r
   __syncthreads();
   int run = incl - sum;
   for (int w = 0; w < warp; ++w) run += s_wsum[w];
-  const int32_t* base = hist + static_cast<int64_t>(blockIdx.x) * n;
   for (int e = e0; e < e1; ++e) {
     if (blockIdx.x == 0) offsets[e] = run;     // offsets[E] = the routed slots
-    int cur = run + __ldg(base + e);
+    int cur = run + s_before[e];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kPlaceWarps; ++w) {
       const int c = s_cur[w * n + e];
       s_cur[w * n + e] = cur;
       cur += c;
     }
-    run += __ldg(totals + e);
+    run += s_total[e];
   }
   __syncthreads();
-  int* cur = s_cur + warp * n;
-#pragma unroll
-  for (int i = 0; i < kPerWarp / 32; ++i) {
-    const int64_t s = w0 + i * 32 + lane;
-    const unsigned same = __match_any_sync(0xffffffffu, key[i]);
+  int* cur = s_cur + (warp < kPlaceWarps ? warp : 0) * n;
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int i = i0 + lane;
+    const int key = i < w1 ? key_of(__ldg(ids + c0 + i), E) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, key);
     const int rank = __popc(same & ((1u << lane) - 1u));
-    const int p = key[i] >= 0 ? cur[key[i]] + rank : 0;
+    const int p = key >= 0 ? cur[key] + rank : 0;
     __syncwarp();
-    if (key[i] >= 0 && rank == 0) cur[key[i]] += __popc(same);
+    if (key >= 0 && rank == 0) cur[key] += __popc(same);
     __syncwarp();
-    if (key[i] >= 0) {
-      slot_pos[s] = key[i] < E ? p : -1 - p;
-      sorted_slot[p] = static_cast<int32_t>(s);
+    if (key >= 0) {
+      slot_pos[c0 + i] = key < E ? p : -1 - p;
+      sorted_slot[p] = c0 + i;
     }
   }
 }
 
-// xs rows of one token per CTA: its x row is read once and written to its k places.
+// xs rows of one token per CTA: its x row is read once and written to its k places.  Tokens that are
+// written at the same time are neighbours, and so are their rows of an expert: with a run of tokens
+// per CTA instead, the same stores of 32768 x 2048 rows, k = 10, took 264 us instead of 236.
 __global__ void __launch_bounds__(kThreads) sort_gather_kernel(const uint4* __restrict__ x,
                                                                const int32_t* __restrict__ slot_pos, int units, int k,
                                                                uint4* __restrict__ xs) {
   __shared__ int s_pos[kMaxK];
   const int64_t t = blockIdx.x;
   const uint4* row = x + t * units;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < units) v = __ldg(row + threadIdx.x);
   pdl_wait();
   if (threadIdx.x < k) s_pos[threadIdx.x] = __ldg(slot_pos + t * k + threadIdx.x);
   __syncthreads();
   for (int u = threadIdx.x; u < units; u += blockDim.x) {
-    const uint4 v = __ldg(row + u);
+    if (u >= blockDim.x) v = __ldg(row + u);
     for (int j = 0; j < k; ++j) {
       const int p = s_pos[j];
       xs[static_cast<int64_t>(p >= 0 ? p : -1 - p) * units + u] = p >= 0 ? v : make_uint4(0, 0, 0, 0);
@@ -370,14 +350,19 @@ int units_of(const SortShape& s) { return s.H * (s.fp32 ? 4 : 2) / 16; }
 
 }  // namespace
 
-int64_t sort_chunks(int64_t S) { return (S + kChunk - 1) / kChunk; }
+// Slots of a chunk, a multiple of 32.
+int chunk_of(int64_t S) {
+  const int64_t c = std::max<int64_t>(kMinChunk, (S + kMaxChunks - 1) / kMaxChunks);
+  return static_cast<int>((c + 31) / 32 * 32);
+}
+int64_t sort_chunks(int64_t S) { return (S + chunk_of(S) - 1) / chunk_of(S); }
 
-// Up to this many slots every CTA counts the ranks itself; above, the counting sort's four launches.
+// Up to this many slots every CTA counts the ranks itself; above, the counting sort's three launches
+// (T = 204, k = 10: 11.8 us, T = 205: 15.4 us).
 constexpr int kRankMaxSlots = 2048;
 
 cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t* ids, void* xs, int32_t* offsets,
-                               int32_t* sorted_slot, int32_t* slot_pos, int32_t* hist, int32_t* totals, int32_t* status,
-                               cudaStream_t st) {
+                               int32_t* sorted_slot, int32_t* slot_pos, int32_t* hist, int32_t* status, cudaStream_t st) {
   const int units = units_of(s);
   const int S = s.T * s.k;
   const uint4* xv = static_cast<const uint4*>(x);
@@ -385,14 +370,14 @@ cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t*
   if (S <= kRankMaxSlots)
     return launch_pdl(true, sort_rank_kernel, dim3(s.T), dim3(kThreads), sizeof(int) * S, st, xv, ids, s.T, units, s.E, s.k,
                       xo, offsets, sorted_slot, slot_pos, status);
-  const int chunks = static_cast<int>(sort_chunks(S));
-  const size_t smem = sizeof(int) * kWarps * (s.E + 1);
-  cudaError_t e = launch_pdl(true, sort_count_kernel, dim3(chunks), dim3(kThreads), 0, st, ids, S, s.E, hist, status);
+  const int chunk = chunk_of(S), chunks = static_cast<int>(sort_chunks(S));
+  const int smem = static_cast<int>(sizeof(int)) * (kPlaceWarps + 2) * (s.E + 1);
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(sort_place_kernel), smem);
   if (e == cudaSuccess)
-    e = launch_pdl(true, sort_scan_kernel, dim3(s.E / 32 + 1), dim3(1024), 0, st, hist, chunks, s.E, totals);
+    e = launch_pdl(true, sort_count_kernel, dim3(chunks), dim3(kSortThreads), 0, st, ids, S, chunk, s.E, hist, status);
   if (e == cudaSuccess)
-    e = launch_pdl(true, sort_place_kernel, dim3(chunks), dim3(kThreads), smem, st, ids, S, s.E,
-                   static_cast<const int32_t*>(hist), static_cast<const int32_t*>(totals), offsets, sorted_slot, slot_pos);
+    e = launch_pdl(true, sort_place_kernel, dim3(chunks), dim3(kSortThreads), smem, st, ids, S, chunk, s.E,
+                   static_cast<const int32_t*>(hist), offsets, sorted_slot, slot_pos);
   if (e == cudaSuccess)
     e = launch_pdl(true, sort_gather_kernel, dim3(s.T), dim3(std::min(kThreads, (units + 31) / 32 * 32)), 0, st, xv,
                    static_cast<const int32_t*>(slot_pos), units, s.k, xo);
