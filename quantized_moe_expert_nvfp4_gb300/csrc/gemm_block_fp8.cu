@@ -9,9 +9,9 @@
 // thread per row) and the matrix's rows its N, so a thread's scale is one number per block and the
 // promotion costs one packed fma per two elements.
 // Per CTA (one per SM, persistent over (row tile, column tile) items):
-//   warp 0      TMA producer of the matrix tiles (32 KB per stage: 256 / BN chunks of K = 128)
+//   warp 0      TMA producer of the matrix tiles, K = 128 per stage
 //   warp 1      MMA issuer
-//   warp 2      TMA producer of the row tiles (boxes of 16 to kRows rows)
+//   warp 2      TMA producer of the row tiles (boxes of 16 to 128 rows)
 //   warp 3      TMEM allocation
 //   warps 4-11  promotion and stores: two warpgroups, half of the tile's columns each
 // An accumulator row that belongs to no row of the tile is fed by whatever shared memory holds and
@@ -37,21 +37,21 @@ constexpr int kChunk = 128;                    // K of a scale block: one 128-by
 constexpr uint32_t kSpinLimit = 1u << 24;      // drain loops only
 constexpr uint64_t kWaitTimeoutNs = 1000000000ull;
 
-// BN: columns of a tile (MMA N); kRows: rows of a tile that a CTA holds at most.  kPair: a cluster of
-// two CTAs takes a tile of 2 kRows rows with one cta_group::2 MMA; each holds its own rows, half of
-// the matrix tile, and the accumulator of its rows.
-template <int BN, int kRows, bool kPair>
+constexpr int kRows = 128;                     // rows of a tile that a CTA holds (its TMEM lanes)
+
+// BN: columns of a tile (MMA N).  kPair: a cluster of two CTAs takes a tile of 256 rows with one
+// cta_group::2 MMA; each holds its own rows, half of the matrix tile, and the accumulator of its rows.
+template <int BN, bool kPair>
 struct Tile {
   static constexpr int kTileRows = kPair ? 2 * kRows : kRows;
   static constexpr int kBRows = kPair ? BN / 2 : BN;           // matrix rows in this CTA's shared memory
-  static constexpr int kChunks = kPair ? 1 : 256 / BN;         // K chunks per stage
-  static constexpr int kAStage = kChunks * kRows * kChunk;
-  static constexpr int kBStage = kChunks * kBRows * kChunk;
+  static constexpr int kAStage = kRows * kChunk;               // a stage is one scale block of K
+  static constexpr int kBStage = kBRows * kChunk;
   static constexpr int kBufs = std::min(4, 512 / BN);          // TMEM accumulators
   static constexpr int kTmemCols = kBufs * BN;
   static constexpr int kCols = BN / kPromoteWgs;               // columns per promoting thread
   static constexpr int kBoxes = kRows / 16;
-  static constexpr int kWarps = kRows / 32 * kPromoteWgs;      // promoting warps with rows
+  static constexpr int kWarps = 4 * kPromoteWgs;               // promoting warps
   static constexpr int kBoxesOut = kCols / 64;                 // staged boxes of 32 rows x 128 bytes per warp
   static constexpr int kStaging = kWarps * kBoxesOut * 4096;
   static constexpr int kStages = std::min(kMaxStages, (220160 - kStaging) / (kAStage + kBStage));
@@ -60,9 +60,8 @@ struct Tile {
 
 template <int kBoxes>
 struct Maps {
-  CUtensorMap a[kBoxes];         // row codes, a box of 16 (i + 1) rows x kChunks chunks
-  CUtensorMap b;                 // matrix codes, kChunks chunks
-  CUtensorMap b_one;             // one chunk
+  CUtensorMap a[kBoxes];         // row codes, a box of 16 (i + 1) rows
+  CUtensorMap b;                 // matrix codes
   CUtensorMap b_tail;            // the last chunk of a K that is no multiple of 128
   CUtensorMap out;               // bf16 output, a box of 32 rows x 64 columns
 };
@@ -269,15 +268,15 @@ struct Items {
   }
 };
 
-template <int BN, int kRows, bool kPair>
+template <int BN, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
-    block_fp8_kernel(const __grid_constant__ Maps<Tile<BN, kRows, kPair>::kBoxes> maps, BlockFp8Args a, bool vec) {
-  using C = Tile<BN, kRows, kPair>;
+    block_fp8_kernel(const __grid_constant__ Maps<Tile<BN, kPair>::kBoxes> maps, BlockFp8Args a, bool vec) {
+  using C = Tile<BN, kPair>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ GroupTiles gt;
   __shared__ Bars sm;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sA = base;                                // row tiles first: reads past a short tile stay inside
+  uint8_t* sA = base;
   uint8_t* sB = base + C::kStages * C::kAStage;
   uint8_t* sOut = sB + C::kStages * C::kBStage;
 
@@ -285,7 +284,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t rank = kPair ? cluster_rank() : 0;    // rank 0 of a pair issues the MMAs
   const int NT = (a.N + BN - 1) / BN;
   const int KB = (a.K + kChunk - 1) / kChunk, KF = a.K / kChunk;
-  const int KS = (KB + C::kChunks - 1) / C::kChunks;   // stages per item
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMaxStages; ++s) {
@@ -330,10 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < kWarpPromote) {
-    // 384 threads launch with 168 registers each: 128 x 40 + 256 x 232 of the same total
-    // (or 88 and 208 of the smaller tile)
-    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // 384 threads launch with 168 registers each; 128 x 32 + 256 x 232 are less than that.  The
+    // promotion must not spill: with 36 bytes of it the dense product took 139 instead of 125 us.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
     if (warp == kWarpTmaB || warp == kWarpTmaA) {
       if (lane == 0) {
         uint32_t is = 0;
@@ -348,23 +345,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           // CTAs' bytes.
           const int box0 = (min(rt.rows, kRows) + 15) >> 4, box1 = (max(rt.rows - kRows, 1) + 15) >> 4;
           const int box = rank == 0 ? box0 : box1;
-          for (int s = 0; s < KS; ++s, ++is) {
-            const int st = is % C::kStages, kb0 = s * C::kChunks;
+          for (int kb = 0; kb < KB; ++kb, ++is) {
+            const int st = is % C::kStages;
             if (!(ok = wait(&sm.empty[st], ((is / C::kStages) & 1) ^ 1))) break;
             const uint32_t bar = kPair ? cluster_addr(&sm.full[st], 0) : smem_u32(&sm.full[st]);
             if (warp == kWarpTmaA) {
-              if (rank == 0) mbar_expect_tx(&sm.full[st], C::kChunks * (box0 + (kPair ? box1 : 0)) * 16 * kChunk);
-              load_3d<kPair>(sA + st * C::kAStage, &maps.a[box - 1], 0, rt.row + static_cast<int>(rank) * kRows, kb0, bar);
-            } else if (kb0 + C::kChunks <= KF) {
+              if (rank == 0) mbar_expect_tx(&sm.full[st], (box0 + (kPair ? box1 : 0)) * 16 * kChunk);
+              load_3d<kPair>(sA + st * C::kAStage, &maps.a[box - 1], 0, rt.row + static_cast<int>(rank) * kRows, kb, bar);
+            } else {
               if (rank == 0) mbar_expect_tx(&sm.full[st], C::kBStage * (kPair ? 2 : 1));
-              load_4d<kPair>(sB + st * C::kBStage, &maps.b, 0, n0, kb0, rt.group, bar);
-            } else {   // the last stage, chunk by chunk
-              if (rank == 0) mbar_expect_tx(&sm.full[st], (KB - kb0) * C::kBRows * kChunk * (kPair ? 2 : 1));
-              for (int kb = kb0; kb < KB; ++kb) {
-                uint8_t* dst = sB + st * C::kBStage + (kb - kb0) * C::kBRows * kChunk;
-                if (kb < KF) load_4d<kPair>(dst, &maps.b_one, 0, n0, kb, rt.group, bar);
-                else load_3d<kPair>(dst, &maps.b_tail, kb * kChunk, n0, rt.group, bar);
-              }
+              if (kb < KF) load_4d<kPair>(sB + st * C::kBStage, &maps.b, 0, n0, kb, rt.group, bar);
+              else load_3d<kPair>(sB + st * C::kBStage, &maps.b_tail, kb * kChunk, n0, rt.group, bar);
             }
           }
         }
@@ -387,29 +378,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t is = 0, ib = 0;
       bool ok = true;
       for (; ok && it.more(); it.next()) {
-        const RowTile rt = group_tile_warp(gt, a.G, it.tile, C::kTileRows, lane);
-        if (rt.group == a.G) continue;
-        const int a_chunk = ((min(rt.rows, kRows) + 15) & ~15) * kChunk;
-        for (int s = 0; ok && s < KS; ++s, ++is) {
-          const int st = is % C::kStages;
+        if (group_tile_warp(gt, a.G, it.tile, C::kTileRows, lane).group == a.G) continue;
+        for (int kb = 0; kb < KB; ++kb, ++is, ++ib) {
+          const int st = is % C::kStages, buf = ib % C::kBufs;
           if (!(ok = warp_wait(&sm.full[st], (is / C::kStages) & 1))) break;
-          const int chunks = min(C::kChunks, KB - s * C::kChunks);
-          for (int c = 0; c < chunks; ++c, ++ib) {
-            const int buf = ib % C::kBufs;
-            if (!(ok = warp_wait(&sm.acc_empty[buf], ((ib / C::kBufs) & 1) ^ 1))) break;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t aa = smem_u32(sA + st * C::kAStage) + c * a_chunk;
-              const uint32_t ba = smem_u32(sB + st * C::kBStage) + c * C::kBRows * kChunk;
+          if (!(ok = warp_wait(&sm.acc_empty[buf], ((ib / C::kBufs) & 1) ^ 1))) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t aa = smem_u32(sA + st * C::kAStage), ba = smem_u32(sB + st * C::kBStage);
 #pragma unroll
-              for (int kk = 0; kk < kChunk / 32; ++kk)
-                mma_e4m3<kPair>(tmem + buf * BN, smem_desc_sw128(aa + kk * 32), smem_desc_sw128(ba + kk * 32), idesc, kk != 0);
-              commit<kPair>(&sm.acc_full[buf]);
-            }
-            __syncwarp();
+            for (int kk = 0; kk < kChunk / 32; ++kk)
+              mma_e4m3<kPair>(tmem + buf * BN, smem_desc_sw128(aa + kk * 32), smem_desc_sw128(ba + kk * 32), idesc, kk != 0);
+            commit<kPair>(&sm.acc_full[buf]);
+            commit<kPair>(&sm.empty[st]);
           }
-          if (!ok) break;
-          if (elect_one()) commit<kPair>(&sm.empty[st]);
           __syncwarp();
         }
       }
@@ -421,16 +403,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else {
-    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int q = warp & 3, wg = (warp - kWarpPromote) >> 2;
-    if (q * 32 < kRows) {
+    {
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + wg * C::kCols;
       const int NB = (a.N + 127) / 128, pitch = (KB + 3) & ~3;
       uint32_t ib = 0;
       bool ok = true;
       const int r0 = static_cast<int>(rank) * kRows + q * 32;   // this warp's first row of the tile
-      uint8_t* stage = sOut + (wg * (kRows / 32) + q) * C::kBoxesOut * 4096;
+      uint8_t* stage = sOut + (wg * 4 + q) * C::kBoxesOut * 4096;
       // an item and its first scales, read before the previous item is stored
       struct Job {
         int group, row0, rows, n0;             // this warp's rows (none or fewer than 32 at a group's end)
@@ -521,10 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BN, int kRows, bool kPair>
+template <int BN, bool kPair>
 cudaError_t launch_tile(const BlockFp8Args& a, int n_sm, cudaStream_t st) {
-  using C = Tile<BN, kRows, kPair>;
-  auto kern = block_fp8_kernel<BN, kRows, kPair>;
+  using C = Tile<BN, kPair>;
+  auto kern = block_fp8_kernel<BN, kPair>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), C::kSmem);
   if (e != cudaSuccess) return e;
   const uint64_t M = a.M, N = a.N, K = a.K, G = a.G, KB = (K + kChunk - 1) / kChunk, KF = K / kChunk;
@@ -532,14 +513,13 @@ cudaError_t launch_tile(const BlockFp8Args& a, int n_sm, cudaStream_t st) {
   bool ok = true;
   for (int i = 0; ok && i < C::kBoxes; ++i) {
     const uint64_t dims[3] = {kChunk, M, KB}, strides[2] = {KB * kChunk, kChunk};
-    const uint32_t box[3] = {kChunk, static_cast<uint32_t>(16 * (i + 1)), C::kChunks};
+    const uint32_t box[3] = {kChunk, static_cast<uint32_t>(16 * (i + 1)), 1};
     ok = make_tensor_map(&maps.a[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.x_codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (ok && KF > 0) {
     const uint64_t dims[4] = {kChunk, N, KF, G}, strides[3] = {K, kChunk, N * K};
-    const uint32_t box[4] = {kChunk, C::kBRows, C::kChunks, 1}, one[4] = {kChunk, C::kBRows, 1, 1};
-    ok = make_tensor_map(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.w_codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) &&
-         make_tensor_map(&maps.b_one, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.w_codes, dims, strides, one, CU_TENSOR_MAP_SWIZZLE_128B);
+    const uint32_t box[4] = {kChunk, C::kBRows, 1, 1};
+    ok = make_tensor_map(&maps.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a.w_codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (ok && K % kChunk) {
     const uint64_t dims[3] = {K, N, G}, strides[2] = {K, N * K};
@@ -580,10 +560,15 @@ cudaError_t launch_block_fp8_matmul(const BlockFp8Args& a, cudaStream_t st) {
   int n_sm = 0;
   cudaError_t e = current_sm_count(&n_sm);
   if (e != cudaSuccess) return e;
-  const int64_t large = (a.M / 128 + std::min<int64_t>(a.M, a.G)) * ((a.N + 255) / 256);
-  if (a.M <= 16 * static_cast<int64_t>(a.G) || large < n_sm) return launch_tile<128, 32, false>(a, n_sm, st);
-  if (a.M >= 256 * static_cast<int64_t>(a.G)) return launch_tile<256, 128, true>(a, n_sm, st);
-  return launch_tile<256, 128, false>(a, n_sm, st);
+  // Tiles of 128 x 256, at most one partial one per group.  Half as wide while half of the SMs would
+  // have none (M = 512, N = K = 4096: 24 against 28 us; M = 1024: 37 against 30 us); pairs of CTAs,
+  // which read a third less from L2, where groups fill their 256 rows and K is long enough for the
+  // pair's start (N = K = 4096: 75 against 80 us at M = 4096; 640 rows per group, N = 2048: 624
+  // against 608 us at K = 512).
+  const int64_t row_tiles = a.G == 1 ? (a.M + kRows - 1) / kRows : a.M / kRows + std::min(a.M, a.G);
+  if (2 * row_tiles * ((a.N + 255) / 256) <= n_sm) return launch_tile<128, false>(a, n_sm, st);
+  if (a.M >= 256 * static_cast<int64_t>(a.G) && a.K >= 1024) return launch_tile<256, true>(a, n_sm, st);
+  return launch_tile<256, false>(a, n_sm, st);
 }
 
 }  // namespace moe
