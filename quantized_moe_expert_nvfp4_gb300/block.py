@@ -62,14 +62,15 @@ def declare(L):
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _ptr(t: torch.Tensor | None, dtype=None, name="tensor"):
-    """The address of a contiguous CUDA tensor of the type, as the package's _ptr checks it (a plain int:
-    a decode step's calls take as long as their Python)."""
+def _arg(t: torch.Tensor | None, shape, dtype, name):
+    """The address of a contiguous CUDA tensor of that shape and type (None for None).  One Python call
+    per tensor: a decode step's calls take as long as their Python."""
     if t is None:
         return None
-    if (dtype is None or t.dtype is dtype) and t.is_cuda and t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
         return t.data_ptr()
-    return _checked_ptr(t, dtype, name)
+    _checked_ptr(t, dtype, name)
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _row_type(t: torch.Tensor, name: str) -> int:
@@ -81,17 +82,8 @@ def _row_type(t: torch.Tensor, name: str) -> int:
     raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
 
 
-def _shaped(t: torch.Tensor | None, shape: tuple, name: str) -> None:
-    if t is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-
-
-def _out(t: torch.Tensor | None, shape: tuple, dtype, like: torch.Tensor, name: str) -> torch.Tensor:
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if t.shape != shape:
-        _shaped(t, shape, name)
-    return t
+def _new(t: torch.Tensor | None, shape, dtype, like: torch.Tensor) -> torch.Tensor:
+    return t if t is not None else torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _ws(fn: str, nbytes: int, device) -> torch.Tensor:
@@ -111,63 +103,56 @@ def sort_tokens(x, topk_ids, E: int, ws, xs=None, offsets=None, sorted_slot=None
     """Rows of x [T, H] (bf16 or fp32) by expert: (xs [T k, H], offsets [E + 1], sorted_slot [T k],
     slot_pos [T, k]).  Slots with a negative id are dropped: their rows come last and are zeros, and
     their slot_pos is -1 - row."""
-    T, H = x.shape
+    rows = x.shape
+    T, H = rows
     k = topk_ids.shape[1]
-    _shaped(topk_ids, (T, k), "topk_ids")
-    S = T * k
-    fp32 = _row_type(x, "x")
-    i32 = _I32
-    xs = _out(xs, (S, H), x.dtype, x, "xs")
-    offsets = _out(offsets, (E + 1,), i32, x, "offsets")
-    sorted_slot = _out(sorted_slot, (S,), i32, x, "sorted_slot")
-    slot_pos = _out(slot_pos, (T, k), i32, x, "slot_pos")
+    dt, slots = x.dtype, (T, k)
+    xs = _new(xs, (T * k, H), dt, x)
+    offsets = _new(offsets, (E + 1,), _I32, x)
+    sorted_slot = _new(sorted_slot, (T * k,), _I32, x)
+    slot_pos = _new(slot_pos, slots, _I32, x)
     _check("moe_sort_tokens", load().moe_sort_tokens(
-        _ptr(x), _ptr(topk_ids, i32, "topk_ids"), MoeTokens(T, H, E, k, fp32), _ptr(xs, x.dtype, "xs"),
-        _ptr(offsets, i32, "offsets"), _ptr(sorted_slot, i32, "sorted_slot"), _ptr(slot_pos, i32, "slot_pos"),
-        _ptr(ws, _U8, "ws"), ws.numel(), _stream(stream)))
+        _arg(x, rows, dt, "x"), _arg(topk_ids, slots, _I32, "topk_ids"), MoeTokens(T, H, E, k, _row_type(x, "x")),
+        _arg(xs, (T * k, H), dt, "xs"), _arg(offsets, (E + 1,), _I32, "offsets"),
+        _arg(sorted_slot, (T * k,), _I32, "sorted_slot"), _arg(slot_pos, slots, _I32, "slot_pos"),
+        _arg(ws, ws.shape, _U8, "ws"), ws.numel(), _stream(stream)))
     return xs, offsets, sorted_slot, slot_pos
-
-
-def _slots(rows, slot_pos, name):
-    T, k = slot_pos.shape
-    H = rows.shape[1]
-    _shaped(rows, (T * k, H), name)
-    return T, k, H, MoeTokens(T, H, 1, k, _row_type(rows, name))
 
 
 def sort_tokens_backward(dxs, slot_pos, dx=None, stream=None):
     """dx [T, H]: for each token the sum of its routed slots' rows of dxs [T k, H]."""
-    T, k, H, shape = _slots(dxs, slot_pos, "dxs")
-    dx = _out(dx, (T, H), dxs.dtype, dxs, "dx")
+    T, k = slots = slot_pos.shape
+    H, dt = dxs.shape[1], dxs.dtype
+    dx = _new(dx, (T, H), dt, dxs)
     _check("moe_sort_tokens_backward", load().moe_sort_tokens_backward(
-        _ptr(dxs), _ptr(slot_pos, _I32, "slot_pos"), shape, _ptr(dx, dxs.dtype, "dx"), _stream(stream)))
+        _arg(dxs, (T * k, H), dt, "dxs"), _arg(slot_pos, slots, _I32, "slot_pos"),
+        MoeTokens(T, H, 1, k, _row_type(dxs, "dxs")), _arg(dx, (T, H), dt, "dx"), _stream(stream)))
     return dx
 
 
 def return_tokens(ys, slot_pos, topk_w, shared=None, out=None, stream=None):
     """out [T, H]: for each token the weighted sum of its routed slots' rows of ys [T k, H], plus its
     row of `shared` [T, H] when given."""
-    T, k, H, shape = _slots(ys, slot_pos, "ys")
-    _shaped(topk_w, (T, k), "topk_w")
-    _shaped(shared, (T, H), "shared")
-    out = _out(out, (T, H), ys.dtype, ys, "out")
+    T, k = slots = slot_pos.shape
+    H, dt = ys.shape[1], ys.dtype
+    out = _new(out, (T, H), dt, ys)
     _check("moe_return_tokens", load().moe_return_tokens(
-        _ptr(ys), _ptr(slot_pos, _I32, "slot_pos"), _ptr(topk_w, _F32, "topk_w"),
-        _ptr(shared, ys.dtype, "shared"), shape, _ptr(out, ys.dtype, "out"), _stream(stream)))
+        _arg(ys, (T * k, H), dt, "ys"), _arg(slot_pos, slots, _I32, "slot_pos"), _arg(topk_w, slots, _F32, "topk_w"),
+        _arg(shared, (T, H), dt, "shared"), MoeTokens(T, H, 1, k, _row_type(ys, "ys")), _arg(out, (T, H), dt, "out"),
+        _stream(stream)))
     return out
 
 
 def return_tokens_backward(dout, ys, slot_pos, topk_w, dys=None, dw=None, stream=None):
     """Gradients (dys [T k, H], dw fp32 [T, k]) of return_tokens; that of `shared` is dout itself."""
-    T, k, H, shape = _slots(ys, slot_pos, "ys")
-    _shaped(dout, (T, H), "dout")
-    _shaped(topk_w, (T, k), "topk_w")
-    dys = _out(dys, (T * k, H), ys.dtype, ys, "dys")
-    dw = _out(dw, (T, k), _F32, ys, "dw")
+    T, k = slots = slot_pos.shape
+    H, dt = ys.shape[1], ys.dtype
+    dys = _new(dys, (T * k, H), dt, ys)
+    dw = _new(dw, slots, _F32, ys)
     _check("moe_return_tokens_backward", load().moe_return_tokens_backward(
-        _ptr(dout, ys.dtype, "dout"), _ptr(ys), _ptr(slot_pos, _I32, "slot_pos"),
-        _ptr(topk_w, _F32, "topk_w"), shape, _ptr(dys, ys.dtype, "dys"), _ptr(dw, _F32, "dw"),
-        _stream(stream)))
+        _arg(dout, (T, H), dt, "dout"), _arg(ys, (T * k, H), dt, "ys"), _arg(slot_pos, slots, _I32, "slot_pos"),
+        _arg(topk_w, slots, _F32, "topk_w"), MoeTokens(T, H, 1, k, _row_type(ys, "ys")),
+        _arg(dys, (T * k, H), dt, "dys"), _arg(dw, slots, _F32, "dw"), _stream(stream)))
     return dys, dw
 
 
@@ -181,27 +166,28 @@ class BlockFP8Weights:
     scales: torch.Tensor
 
     def c(self) -> MoeBlockFp8Weights:
-        G, N, K = self.codes.shape
-        _shaped(self.scales, (G, -(-N // 128), -(-K // 128)), "scales")
-        return MoeBlockFp8Weights(_ptr(self.codes, _U8, "codes"), _ptr(self.scales, _F32, "scales"), G, N, K)
+        G, N, K = shape = self.codes.shape
+        return MoeBlockFp8Weights(_arg(self.codes, shape, _U8, "codes"),
+                                  _arg(self.scales, (G, -(-N // 128), -(-K // 128)), _F32, "scales"), G, N, K)
 
 
 def quantize_block_fp8(w: torch.Tensor, stream=None) -> BlockFP8Weights:
     """Load-time quantization of fp32 or bf16 matrices [G, N, K]."""
     G, N, K = w.shape
-    codes = torch.empty(G, N, K, dtype=torch.uint8, device=w.device)
-    scales = torch.empty(G, -(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
+    q = BlockFP8Weights(torch.empty(G, N, K, dtype=_U8, device=w.device),
+                        torch.empty(G, -(-N // 128), -(-K // 128), dtype=_F32, device=w.device))
     _check("moe_quantize_block_fp8", load().moe_quantize_block_fp8(
-        _ptr(w), _row_type(w, "w"), G, N, K, _ptr(codes), _ptr(scales), _stream(stream)))
-    return BlockFP8Weights(codes, scales)
+        _arg(w, w.shape, w.dtype, "w"), _row_type(w, "w"), G, N, K, q.codes.data_ptr(), q.scales.data_ptr(), _stream(stream)))
+    return q
 
 
 def transpose_block_fp8(w: BlockFP8Weights, stream=None) -> BlockFP8Weights:
     """The transposed matrices [G, K, N] (the same values), for the gradient of the product."""
     G, N, K = w.codes.shape
-    t = BlockFP8Weights(torch.empty(G, K, N, dtype=torch.uint8, device=w.codes.device),
-                        torch.empty(G, -(-K // 128), -(-N // 128), dtype=torch.float32, device=w.codes.device))
-    _check("moe_transpose_block_fp8", load().moe_transpose_block_fp8(w.c(), _ptr(t.codes), _ptr(t.scales), _stream(stream)))
+    t = BlockFP8Weights(torch.empty(G, K, N, dtype=_U8, device=w.codes.device),
+                        torch.empty(G, -(-K // 128), -(-N // 128), dtype=_F32, device=w.codes.device))
+    _check("moe_transpose_block_fp8", load().moe_transpose_block_fp8(
+        w.c(), t.codes.data_ptr(), t.scales.data_ptr(), _stream(stream)))
     return t
 
 
@@ -209,10 +195,10 @@ def quantize_rows_block_fp8(x: torch.Tensor, stream=None):
     """bf16 [rows, K] -> (codes u8 [rows, 128 KB], scales fp32 [rows, KB rounded up to 4]), KB = ceil(K / 128)."""
     rows, K = x.shape
     KB = -(-K // 128)
-    codes = torch.empty(rows, 128 * KB, dtype=torch.uint8, device=x.device)
-    scales = torch.empty(rows, -(-KB // 4) * 4, dtype=torch.float32, device=x.device)
+    codes = torch.empty(rows, 128 * KB, dtype=_U8, device=x.device)
+    scales = torch.empty(rows, -(-KB // 4) * 4, dtype=_F32, device=x.device)
     _check("moe_quantize_rows_block_fp8", load().moe_quantize_rows_block_fp8(
-        _ptr(x, _BF16, "x"), rows, K, _ptr(codes), _ptr(scales), _stream(stream)))
+        _arg(x, x.shape, _BF16, "x"), rows, K, codes.data_ptr(), scales.data_ptr(), _stream(stream)))
     return codes, scales
 
 
@@ -226,17 +212,14 @@ def block_fp8_matmul(x, w: BlockFP8Weights, ws, offsets=None, out=None, out_fp32
     """x bf16 [M, K] quantized in blocks of 128 times the matrices: out [M, N] bf16 or fp32 (the type
     of `out`, when given).  offsets int32 [G + 1] (sort_tokens's): rows of each matrix; rows past the
     last are zeros.  Without offsets, one matrix (G = 1) for all rows."""
-    M, K = x.shape
+    M, K = rows = x.shape
     G, N, wk = w.codes.shape
     if K != wk:
         raise ValueError(f"x has {K} columns, the matrices {wk}")
-    _shaped(offsets, (G + 1,), "offsets")
-    if out is None:
-        out = torch.empty(M, N, dtype=torch.float32 if out_fp32 else torch.bfloat16, device=x.device)
-    _shaped(out, (M, N), "out")
+    out = _new(out, (M, N), _F32 if out_fp32 else _BF16, x)
     _check("moe_block_fp8_matmul", load().moe_block_fp8_matmul(
-        _ptr(x, _BF16, "x"), M, _ptr(offsets, _I32, "offsets"), w.c(), _ptr(out), _row_type(out, "out"),
-        _ptr(ws, _U8, "ws"), ws.numel(), _stream(stream)))
+        _arg(x, rows, _BF16, "x"), M, _arg(offsets, (G + 1,), _I32, "offsets"), w.c(),
+        _arg(out, (M, N), out.dtype, "out"), _row_type(out, "out"), _arg(ws, ws.shape, _U8, "ws"), ws.numel(), _stream(stream)))
     return out
 
 
@@ -254,41 +237,37 @@ def _gate(gate, T, H):
         return GATE_NONE, None
     shape = gate.shape
     if shape == (H,):
-        return GATE_CHANNEL, torch.float32
+        return GATE_CHANNEL, _F32
     if shape in ((T,), (T, 1)):
-        return GATE_TOKEN, torch.float32
+        return GATE_TOKEN, _F32
     if shape == (T, H):
-        return GATE_ELEMENT, torch.bfloat16
+        return GATE_ELEMENT, _BF16
     raise ValueError(f"gate must have shape ({H},), ({T},), ({T}, 1) or ({T}, {H}), got {tuple(shape)}")
 
 
 def norm_before(x, weight, eps: float = 1e-6, weight_offset: float = 0.0, n=None, rstd=None, stream=None):
     """(n bf16 [T, H], rstd fp32 [T]) of x [T, H] (bf16 or fp32): n = x rstd (weight + weight_offset)."""
-    T, H = x.shape
-    _shaped(weight, (H,), "weight")
-    n = _out(n, (T, H), _BF16, x, "n")
-    rstd = _out(rstd, (T,), _F32, x, "rstd")
+    T, H = rows = x.shape
+    n = _new(n, rows, _BF16, x)
+    rstd = _new(rstd, (T,), _F32, x)
     _check("moe_norm_before", load().moe_norm_before(
-        _ptr(x), _ptr(weight, _F32, "weight"),
-        MoeNorm(T, H, _row_type(x, "x"), 0, GATE_NONE, eps, weight_offset, 1.0, 1.0), _ptr(n, _BF16, "n"),
-        _ptr(rstd, _F32, "rstd"), _stream(stream)))
+        _arg(x, rows, x.dtype, "x"), _arg(weight, (H,), _F32, "weight"),
+        MoeNorm(T, H, _row_type(x, "x"), 0, GATE_NONE, eps, weight_offset, 1.0, 1.0), _arg(n, rows, _BF16, "n"),
+        _arg(rstd, (T,), _F32, "rstd"), _stream(stream)))
     return n, rstd
 
 
 def norm_before_backward(dn, x, weight, rstd, ws, dresidual=None, weight_offset: float = 0.0, dx=None, dw=None, stream=None):
     """(dx, dw) of norm_before; dresidual (x's type) is added to dx."""
-    T, H = x.shape
-    rows, cols, f32 = x.shape, (H,), _F32
-    _shaped(dn, rows, "dn")
-    _shaped(weight, cols, "weight")
-    _shaped(rstd, (T,), "rstd")
-    _shaped(dresidual, rows, "dresidual")
-    dx = _out(dx, (T, H), x.dtype, x, "dx")
-    dw = _out(dw, (H,), f32, x, "dw")
+    T, H = rows = x.shape
+    cols, dt = (H,), x.dtype
+    dx = _new(dx, rows, dt, x)
+    dw = _new(dw, cols, _F32, x)
     _check("moe_norm_before_backward", load().moe_norm_before_backward(
-        _ptr(dn, _BF16, "dn"), _ptr(x), _ptr(weight, f32, "weight"), _ptr(rstd, f32, "rstd"),
-        _ptr(dresidual, x.dtype, "dresidual"), MoeNorm(T, H, _row_type(x, "x"), 0, GATE_NONE, 0.0, weight_offset, 1.0, 1.0),
-        _ptr(dx, x.dtype, "dx"), _ptr(dw, f32, "dw"), _ptr(ws, _U8, "ws"), ws.numel(), _stream(stream)))
+        _arg(dn, rows, _BF16, "dn"), _arg(x, rows, dt, "x"), _arg(weight, cols, _F32, "weight"),
+        _arg(rstd, (T,), _F32, "rstd"), _arg(dresidual, rows, dt, "dresidual"),
+        MoeNorm(T, H, _row_type(x, "x"), 0, GATE_NONE, 0.0, weight_offset, 1.0, 1.0), _arg(dx, rows, dt, "dx"),
+        _arg(dw, cols, _F32, "dw"), _arg(ws, ws.shape, _U8, "ws"), ws.numel(), _stream(stream)))
     return dx, dw
 
 
@@ -296,24 +275,22 @@ def norm_after(y, x, weight, gate=None, w_next=None, residual_scale: float = 1.0
                eps: float = 1e-6, weight_offset: float = 0.0, out=None, n=None, rstd=None, rstd_next=None, stream=None):
     """out = residual_scale x + branch_scale gate (rms(y) weight), and with w_next the next block's norm
     n of the stored out: (out, n or None, rstd, rstd_next or None)."""
-    T, H = x.shape
+    T, H = rows = x.shape
+    cols, dt = (H,), x.dtype
     kind, gate_type = _gate(gate, T, H)
-    rows, cols, f32 = x.shape, (H,), _F32
-    _shaped(y, rows, "y")
-    _shaped(weight, cols, "weight")
-    _shaped(w_next, cols, "w_next")
-    out = _out(out, (T, H), x.dtype, x, "out")
-    rstd = _out(rstd, (T,), f32, x, "rstd")
+    out = _new(out, rows, dt, x)
+    rstd = _new(rstd, (T,), _F32, x)
     if w_next is not None:
-        n = _out(n, (T, H), _BF16, x, "n")
-        rstd_next = _out(rstd_next, (T,), f32, x, "rstd_next")
+        n = _new(n, rows, _BF16, x)
+        rstd_next = _new(rstd_next, (T,), _F32, x)
     elif n is not None or rstd_next is not None:
         raise ValueError("n and rstd_next are outputs of the next norm: they need w_next")
     _check("moe_norm_after", load().moe_norm_after(
-        _ptr(y), _ptr(x), _ptr(weight, f32, "weight"), _ptr(gate, gate_type, "gate"), _ptr(w_next, f32, "w_next"),
+        _arg(y, rows, y.dtype, "y"), _arg(x, rows, dt, "x"), _arg(weight, cols, _F32, "weight"),
+        None if gate is None else _arg(gate, gate.shape, gate_type, "gate"), _arg(w_next, cols, _F32, "w_next"),
         MoeNorm(T, H, _row_type(x, "x"), _row_type(y, "y"), kind, eps, weight_offset, residual_scale, branch_scale),
-        _ptr(out, x.dtype, "out"), _ptr(n, _BF16, "n"), _ptr(rstd, f32, "rstd"), _ptr(rstd_next, f32, "rstd_next"),
-        _stream(stream)))
+        _arg(out, rows, dt, "out"), _arg(n, rows, _BF16, "n"), _arg(rstd, (T,), _F32, "rstd"),
+        _arg(rstd_next, (T,), _F32, "rstd_next"), _stream(stream)))
     return out, n, rstd, rstd_next
 
 
@@ -322,33 +299,31 @@ def norm_after_backward(dout, y, weight, rstd, ws, gate=None, dn=None, out=None,
                         dw=None, dgate=None, dw_next=None, stream=None):
     """(dy, dx, dw, dgate or None, dw_next or None) of norm_after.  With the fused next norm, dn is the
     gradient of its output and `out` the stored output of the forward call."""
-    T, H = y.shape
+    T, H = rows = y.shape
+    cols, dt, yt = (H,), dout.dtype, y.dtype
     kind, gate_type = _gate(gate, T, H)
     nexts = (dn, out, w_next, rstd_next)
     if any(t is None for t in nexts) and any(t is not None for t in nexts):
         raise ValueError("dn, out, w_next and rstd_next belong to the next norm: give all of them or none")
-    rows, cols, f32 = y.shape, (H,), _F32
-    for t, name in ((dout, "dout"), (dn, "dn"), (out, "out")):
-        _shaped(t, rows, name)
-    _shaped(weight, cols, "weight")
-    _shaped(w_next, cols, "w_next")
-    _shaped(rstd, (T,), "rstd")
-    _shaped(rstd_next, (T,), "rstd_next")
-    dy = _out(dy, (T, H), y.dtype, y, "dy")
-    dx = _out(dx, (T, H), dout.dtype, dout, "dx")
-    dw = _out(dw, (H,), f32, y, "dw")
-    if gate is not None:
-        dgate = _out(dgate, tuple(gate.shape), gate_type, y, "dgate")
-    if w_next is not None:
-        dw_next = _out(dw_next, (H,), f32, y, "dw_next")
     if (gate is None and dgate is not None) or (w_next is None and dw_next is not None):
         raise ValueError("dgate needs gate, dw_next needs w_next")
+    dy = _new(dy, rows, yt, y)
+    dx = _new(dx, rows, dt, dout)
+    dw = _new(dw, cols, _F32, y)
+    gate_shape = None
+    if gate is not None:
+        gate_shape = gate.shape
+        dgate = _new(dgate, gate_shape, gate_type, y)
+    if w_next is not None:
+        dw_next = _new(dw_next, cols, _F32, y)
     _check("moe_norm_after_backward", load().moe_norm_after_backward(
-        _ptr(dout), _ptr(dn, _BF16, "dn"), _ptr(y), _ptr(out, dout.dtype, "out"), _ptr(weight, f32, "weight"),
-        _ptr(gate, gate_type, "gate"), _ptr(w_next, f32, "w_next"), _ptr(rstd, f32, "rstd"), _ptr(rstd_next, f32, "rstd_next"),
+        _arg(dout, rows, dt, "dout"), _arg(dn, rows, _BF16, "dn"), _arg(y, rows, yt, "y"), _arg(out, rows, dt, "out"),
+        _arg(weight, cols, _F32, "weight"), _arg(gate, gate_shape, gate_type, "gate"), _arg(w_next, cols, _F32, "w_next"),
+        _arg(rstd, (T,), _F32, "rstd"), _arg(rstd_next, (T,), _F32, "rstd_next"),
         MoeNorm(T, H, _row_type(dout, "dout"), _row_type(y, "y"), kind, 0.0, weight_offset, residual_scale, branch_scale),
-        _ptr(dy, y.dtype, "dy"), _ptr(dx, dout.dtype, "dx"), _ptr(dw, f32, "dw"), _ptr(dgate, gate_type, "dgate"),
-        _ptr(dw_next, f32, "dw_next"), _ptr(ws, _U8, "ws"), ws.numel(), _stream(stream)))
+        _arg(dy, rows, yt, "dy"), _arg(dx, rows, dt, "dx"), _arg(dw, cols, _F32, "dw"),
+        _arg(dgate, gate_shape, gate_type, "dgate"), _arg(dw_next, cols, _F32, "dw_next"),
+        _arg(ws, ws.shape, _U8, "ws"), ws.numel(), _stream(stream)))
     return dy, dx, dw, dgate, dw_next
 
 

@@ -328,9 +328,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp < kWarpPromote) {
-    // 384 threads launch with 168 registers each; 128 x 32 + 256 x 232 are less than that.  The
-    // promotion must not spill: with 36 bytes of it the dense product took 139 instead of 125 us.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+    // 384 threads launch with 168 registers each, 64512 in all: 128 x 32 + 256 x 232 (or 128 x 88 +
+    // 256 x 208 where a thread promotes 64 columns) fit and compile without spills.  With 36 bytes
+    // spilled the dense product took 139 instead of 125 us.
+    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpTmaB || warp == kWarpTmaA) {
       if (lane == 0) {
         uint32_t is = 0;
@@ -403,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int q = warp & 3, wg = (warp - kWarpPromote) >> 2;
     {
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + wg * C::kCols;

@@ -115,24 +115,44 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t*
   int* s_total = s_cur + kPlaceWarps * n;
   int* s_before = s_total + n;
   const int c0 = blockIdx.x * chunk, slots = min(chunk, S - c0);
-  for (int i = threadIdx.x; i < kPlaceWarps * n; i += kSortThreads) s_cur[i] = 0;
+  for (int i = threadIdx.x; i < (kPlaceWarps + 2) * n; i += kSortThreads) s_cur[i] = 0;
   __syncthreads();
   const int run_len = ((slots + kPlaceWarps - 1) / kPlaceWarps + 31) & ~31;
   const int w0 = min(slots, warp * run_len), w1 = warp < kPlaceWarps ? min(slots, w0 + run_len) : w0;
   // ids are older than the counting launch, hist is its result
+#pragma unroll 4
   for (int i = w0 + lane; i < w1; i += 32) atomicAdd(&s_cur[warp * n + key_of(__ldg(ids + c0 + i), E)], 1);
   pdl_wait_then_release();
-  for (int e = threadIdx.x; e < n; e += kSortThreads) {
-    int total = 0, before = 0;
+  {   // the experts' counts in all chunks and in those before this one, several threads per expert;
+      // the last warp adds up the dropped slots
+    const int parts = max(1, kSortThreads / E), part = threadIdx.x / E;
     const int chunks = gridDim.x, mine = blockIdx.x;
+    if (part < parts) {
+      const int e = threadIdx.x - part * E;
+      int total = 0, before = 0;
 #pragma unroll 16
-    for (int c = 0; c < chunks; ++c) {
-      const int v = __ldg(hist + static_cast<int64_t>(c) * n + e);
-      total += v;
-      before += c < mine ? v : 0;
+      for (int c = part; c < chunks; c += parts) {
+        const int v = __ldg(hist + static_cast<int64_t>(c) * n + e);
+        total += v;
+        before += c < mine ? v : 0;
+      }
+      atomicAdd(&s_total[e], total);
+      atomicAdd(&s_before[e], before);
     }
-    s_total[e] = total;
-    s_before[e] = before;
+    if (warp == kSortThreads / 32 - 1) {
+      int total = 0, before = 0;
+      for (int c = lane; c < chunks; c += 32) {
+        const int v = __ldg(hist + static_cast<int64_t>(c) * n + E);
+        total += v;
+        before += c < mine ? v : 0;
+      }
+      total = __reduce_add_sync(0xffffffffu, total);
+      before = __reduce_add_sync(0xffffffffu, before);
+      if (lane == 0) {
+        s_total[E] = total;
+        s_before[E] = before;
+      }
+    }
   }
   __syncthreads();
   // exclusive prefix of the totals: a run of keys per thread
@@ -179,24 +199,26 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const int32_t*
   }
 }
 
-// xs rows of one token per CTA: its x row is read once and written to its k places.  Tokens that are
-// written at the same time are neighbours, and so are their rows of an expert: with a run of tokens
-// per CTA instead, the same stores of 32768 x 2048 rows, k = 10, took 264 us instead of 236.
+// A token's x row is read once, by one group of threads (threadIdx.y), and written to its k places.
+// Tokens that are written at the same time are neighbours, and so are their rows of an expert: with
+// a run of tokens per CTA instead, the same stores of 32768 x 2048 rows, k = 10, took 264 us instead
+// of 236.
 __global__ void __launch_bounds__(kThreads) sort_gather_kernel(const uint4* __restrict__ x,
-                                                               const int32_t* __restrict__ slot_pos, int units, int k,
+                                                               const int32_t* __restrict__ slot_pos, int T, int units, int k,
                                                                uint4* __restrict__ xs) {
-  __shared__ int s_pos[kMaxK];
-  const int64_t t = blockIdx.x;
+  __shared__ int s_pos[kWarps][kMaxK];
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const uint4* row = x + t * units;
   uint4 v = make_uint4(0, 0, 0, 0);
-  if (threadIdx.x < units) v = __ldg(row + threadIdx.x);
+  if (t < T && threadIdx.x < units) v = __ldg(row + threadIdx.x);
   pdl_wait();
-  if (threadIdx.x < k) s_pos[threadIdx.x] = __ldg(slot_pos + t * k + threadIdx.x);
+  if (t < T && threadIdx.x < k) s_pos[threadIdx.y][threadIdx.x] = __ldg(slot_pos + t * k + threadIdx.x);
   __syncthreads();
+  if (t >= T) return;
   for (int u = threadIdx.x; u < units; u += blockDim.x) {
     if (u >= blockDim.x) v = __ldg(row + u);
     for (int j = 0; j < k; ++j) {
-      const int p = s_pos[j];
+      const int p = s_pos[threadIdx.y][j];
       xs[static_cast<int64_t>(p >= 0 ? p : -1 - p) * units + u] = p >= 0 ? v : make_uint4(0, 0, 0, 0);
     }
   }
@@ -301,49 +323,59 @@ __global__ void __launch_bounds__(kThreads) return_kernel(const uint4* __restric
   out[idx] = Elems<V>::put(acc);
 }
 
-// The gradient of the weighted return, one CTA per token: for each rank the row w dout[t] (zeros
-// for a dropped slot) and the dot product of dout[t] with the rank's row.
-template <typename V>
+// The gradient of the weighted return, TX threads per token: for each rank the row w dout[t] (zeros
+// for a dropped slot) and the dot product of dout[t] with the rank's row.  One rank at a time in few
+// registers, and so eight CTAs per SM: two ranks at a time took 504 instead of 452 us
+// (32768 x 2048, k = 10).
+template <typename V, int TX>
 __global__ void __launch_bounds__(kThreads) return_grad_kernel(const uint4* __restrict__ dout,
                                                                const uint4* __restrict__ ys,
                                                                const int32_t* __restrict__ slot_pos,
                                                                const float* __restrict__ w, int64_t T, int units, int k,
                                                                uint4* __restrict__ dys, float* __restrict__ dw) {
-  constexpr int n = Elems<V>::n;
-  __shared__ float s_dot[kMaxK][kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t t = blockIdx.x, S = T * k;
+  constexpr int n = Elems<V>::n, TY = kThreads / TX, kTokenWarps = TX / 32;
+  __shared__ float s_dot[TY][kMaxK][kTokenWarps];
+  const int x = threadIdx.x % TX, y = threadIdx.x / TX, lane = threadIdx.x & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * TY + y, S = T * k;
   pdl_wait();
-  for (int j = 0; j < k; ++j) {
-    const int raw = __ldg(slot_pos + t * k + j);
-    const int p = routed_row(raw, S, nullptr);
-    const int place = p >= 0 ? p : -1 - raw;   // the zero row of a dropped slot (skipped if it is out of range)
-    const float wj = p >= 0 ? __ldg(w + t * k + j) : 0.0f;
-    float dot = 0.0f;
-    for (int u = threadIdx.x; u < units; u += kThreads) {
-      float d[n], r[n];
-      Elems<V>::get(__ldg(dout + t * units + u), d);
-      if (p >= 0) {
-        float y[n];
-        Elems<V>::get(__ldg(ys + static_cast<int64_t>(p) * units + u), y);
+  if (t < T) {
+    for (int j = 0; j < k; ++j) {
+      const int raw = __ldg(slot_pos + t * k + j);
+      const int p = routed_row(raw, S, nullptr);
+      const int place = p >= 0 ? p : -1 - raw;   // the zero row of a dropped slot (skipped if it is out of range)
+      const float wj = p >= 0 ? __ldg(w + t * k + j) : 0.0f;
+      float dot = 0.0f;
+      for (int u = x; u < units; u += TX) {
+        float d[n], r[n];
+        Elems<V>::get(__ldg(dout + t * units + u), d);
+        if (p >= 0) {
+          float v[n];
+          Elems<V>::get(__ldg(ys + static_cast<int64_t>(p) * units + u), v);
 #pragma unroll
-        for (int c = 0; c < n; ++c) dot = fmaf(d[c], y[c], dot);
+          for (int c = 0; c < n; ++c) dot = fmaf(d[c], v[c], dot);
+        }
+#pragma unroll
+        for (int c = 0; c < n; ++c) r[c] = p >= 0 ? wj * d[c] : 0.0f;
+        if (place >= 0 && place < S) dys[static_cast<int64_t>(place) * units + u] = Elems<V>::put(r);
       }
 #pragma unroll
-      for (int c = 0; c < n; ++c) r[c] = p >= 0 ? wj * d[c] : 0.0f;
-      if (place >= 0 && place < S) dys[static_cast<int64_t>(place) * units + u] = Elems<V>::put(r);
+      for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+      if (lane == 0) s_dot[y][j][x / 32] = dot;
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-    if (lane == 0) s_dot[j][warp] = dot;
   }
   __syncthreads();
-  if (threadIdx.x < k) {
+  if (t < T && x < k) {
     float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) v += s_dot[threadIdx.x][i];
-    dw[t * k + threadIdx.x] = v;
+    for (int i = 0; i < kTokenWarps; ++i) v += s_dot[y][x][i];
+    dw[t * k + x] = v;
   }
+}
+
+// Threads of a token's row (a multiple of 32, one per unit up to kThreads) x tokens of a CTA.
+dim3 token_block(int units) {
+  const int warps = std::min(kWarps, (units + 31) / 32);
+  return dim3(32 * warps, kWarps / warps);
 }
 
 int units_of(const SortShape& s) { return s.H * (s.fp32 ? 4 : 2) / 16; }
@@ -370,6 +402,7 @@ cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t*
   if (S <= kRankMaxSlots)
     return launch_pdl(true, sort_rank_kernel, dim3(s.T), dim3(kThreads), sizeof(int) * S, st, xv, ids, s.T, units, s.E, s.k,
                       xo, offsets, sorted_slot, slot_pos, status);
+  const dim3 block = token_block(units);
   const int chunk = chunk_of(S), chunks = static_cast<int>(sort_chunks(S));
   const int smem = static_cast<int>(sizeof(int)) * (kPlaceWarps + 2) * (s.E + 1);
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(sort_place_kernel), smem);
@@ -379,8 +412,8 @@ cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t*
     e = launch_pdl(true, sort_place_kernel, dim3(chunks), dim3(kSortThreads), smem, st, ids, S, chunk, s.E,
                    static_cast<const int32_t*>(hist), offsets, sorted_slot, slot_pos);
   if (e == cudaSuccess)
-    e = launch_pdl(true, sort_gather_kernel, dim3(s.T), dim3(std::min(kThreads, (units + 31) / 32 * 32)), 0, st, xv,
-                   static_cast<const int32_t*>(slot_pos), units, s.k, xo);
+    e = launch_pdl(true, sort_gather_kernel, dim3((s.T + block.y - 1) / block.y), block, 0, st, xv,
+                   static_cast<const int32_t*>(slot_pos), s.T, units, s.k, xo);
   return e;
 }
 
@@ -397,10 +430,15 @@ cudaError_t launch_return_tokens(const SortShape& s, const void* rows, const int
 cudaError_t launch_return_tokens_grad(const SortShape& s, const void* dout, const void* ys, const int32_t* slot_pos,
                                       const float* w, void* dys, float* dw, cudaStream_t st) {
   const int units = units_of(s);
-  auto kern = s.fp32 ? return_grad_kernel<float> : return_grad_kernel<uint16_t>;
-  return launch_pdl(true, kern, dim3(s.T), dim3(kThreads), 0, st, static_cast<const uint4*>(dout),
-                    static_cast<const uint4*>(ys), slot_pos, w, static_cast<int64_t>(s.T), units, s.k,
-                    static_cast<uint4*>(dys), dw);
+  auto launch = [&](auto kern, int tokens) {
+    return launch_pdl(true, kern, dim3((s.T + tokens - 1) / tokens), dim3(kThreads), 0, st, static_cast<const uint4*>(dout),
+                      static_cast<const uint4*>(ys), slot_pos, w, static_cast<int64_t>(s.T), units, s.k,
+                      static_cast<uint4*>(dys), dw);
+  };
+  if (units <= 32) return launch(s.fp32 ? return_grad_kernel<float, 32> : return_grad_kernel<uint16_t, 32>, 8);
+  if (units <= 64) return launch(s.fp32 ? return_grad_kernel<float, 64> : return_grad_kernel<uint16_t, 64>, 4);
+  if (units <= 128) return launch(s.fp32 ? return_grad_kernel<float, 128> : return_grad_kernel<uint16_t, 128>, 2);
+  return launch(s.fp32 ? return_grad_kernel<float, 256> : return_grad_kernel<uint16_t, 256>, 1);
 }
 
 }  // namespace moe
