@@ -324,10 +324,11 @@ __global__ void __launch_bounds__(kThreads) return_kernel(const uint4* __restric
 }
 
 // The gradient of the weighted return, TX threads per token: for each rank the row w dout[t] (zeros
-// for a dropped slot) and the dot product of dout[t] with the rank's row.  One rank at a time in few
-// registers, and so eight CTAs per SM: two ranks at a time took 504 instead of 452 us
-// (32768 x 2048, k = 10).
-template <typename V, int TX>
+// for a dropped slot) and the dot product of dout[t] with the rank's row.  kTogether ranks have their
+// rows in flight at a time: one where many tokens keep HBM busy (in few registers, eight CTAs per SM;
+// two at a time took 504 instead of 452 us for 32768 x 2048, k = 10), four where a token's own
+// latency counts.
+template <typename V, int TX, int kTogether>
 __global__ void __launch_bounds__(kThreads) return_grad_kernel(const uint4* __restrict__ dout,
                                                                const uint4* __restrict__ ys,
                                                                const int32_t* __restrict__ slot_pos,
@@ -339,28 +340,45 @@ __global__ void __launch_bounds__(kThreads) return_grad_kernel(const uint4* __re
   const int64_t t = static_cast<int64_t>(blockIdx.x) * TY + y, S = T * k;
   pdl_wait();
   if (t < T) {
-    for (int j = 0; j < k; ++j) {
-      const int raw = __ldg(slot_pos + t * k + j);
-      const int p = routed_row(raw, S, nullptr);
-      const int place = p >= 0 ? p : -1 - raw;   // the zero row of a dropped slot (skipped if it is out of range)
-      const float wj = p >= 0 ? __ldg(w + t * k + j) : 0.0f;
-      float dot = 0.0f;
+    for (int j0 = 0; j0 < k; j0 += kTogether) {
+      int p[kTogether], place[kTogether];
+      float wj[kTogether], dot[kTogether];
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) {
+        const bool rank = kTogether == 1 || j0 + i < k;
+        const int raw = rank ? __ldg(slot_pos + t * k + j0 + i) : 0;
+        p[i] = rank ? routed_row(raw, S, nullptr) : -1;
+        place[i] = p[i] >= 0 ? p[i] : -1 - raw;   // the zero row of a dropped slot (skipped if it is out of range)
+        if (!rank || place[i] >= S) place[i] = -1;
+        wj[i] = p[i] >= 0 ? __ldg(w + t * k + j0 + i) : 0.0f;
+        dot[i] = 0.0f;
+      }
       for (int u = x; u < units; u += TX) {
-        float d[n], r[n];
+        uint4 q[kTogether];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i)
+          if (p[i] >= 0) q[i] = __ldg(ys + static_cast<int64_t>(p[i]) * units + u);
+        float d[n];
         Elems<V>::get(__ldg(dout + t * units + u), d);
-        if (p >= 0) {
-          float v[n];
-          Elems<V>::get(__ldg(ys + static_cast<int64_t>(p) * units + u), v);
 #pragma unroll
-          for (int c = 0; c < n; ++c) dot = fmaf(d[c], v[c], dot);
+        for (int i = 0; i < kTogether; ++i) {
+          float r[n];
+          if (p[i] >= 0) {
+            Elems<V>::get(q[i], r);
+#pragma unroll
+            for (int c = 0; c < n; ++c) dot[i] = fmaf(d[c], r[c], dot[i]);
+          }
+#pragma unroll
+          for (int c = 0; c < n; ++c) r[c] = p[i] >= 0 ? wj[i] * d[c] : 0.0f;
+          if (place[i] >= 0) dys[static_cast<int64_t>(place[i]) * units + u] = Elems<V>::put(r);
         }
-#pragma unroll
-        for (int c = 0; c < n; ++c) r[c] = p >= 0 ? wj * d[c] : 0.0f;
-        if (place >= 0 && place < S) dys[static_cast<int64_t>(place) * units + u] = Elems<V>::put(r);
       }
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-      if (lane == 0) s_dot[y][j][x / 32] = dot;
+      for (int i = 0; i < kTogether; ++i) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], d);
+        if (lane == 0 && (kTogether == 1 || j0 + i < k)) s_dot[y][j0 + i][x / 32] = dot[i];
+      }
     }
   }
   __syncthreads();
@@ -430,15 +448,23 @@ cudaError_t launch_return_tokens(const SortShape& s, const void* rows, const int
 cudaError_t launch_return_tokens_grad(const SortShape& s, const void* dout, const void* ys, const int32_t* slot_pos,
                                       const float* w, void* dys, float* dw, cudaStream_t st) {
   const int units = units_of(s);
-  auto launch = [&](auto kern, int tokens) {
-    return launch_pdl(true, kern, dim3((s.T + tokens - 1) / tokens), dim3(kThreads), 0, st, static_cast<const uint4*>(dout),
-                      static_cast<const uint4*>(ys), slot_pos, w, static_cast<int64_t>(s.T), units, s.k,
-                      static_cast<uint4*>(dys), dw);
+  int n_sm = 0;
+  cudaError_t e = current_sm_count(&n_sm);
+  if (e != cudaSuccess) return e;
+  auto launch = [&](auto one, auto four, int tokens) {   // tokens of a CTA
+    const int ctas = (s.T + tokens - 1) / tokens;
+    return launch_pdl(true, ctas <= 4 * n_sm ? four : one, dim3(ctas), dim3(kThreads), 0, st,
+                      static_cast<const uint4*>(dout), static_cast<const uint4*>(ys), slot_pos, w,
+                      static_cast<int64_t>(s.T), units, s.k, static_cast<uint4*>(dys), dw);
   };
-  if (units <= 32) return launch(s.fp32 ? return_grad_kernel<float, 32> : return_grad_kernel<uint16_t, 32>, 8);
-  if (units <= 64) return launch(s.fp32 ? return_grad_kernel<float, 64> : return_grad_kernel<uint16_t, 64>, 4);
-  if (units <= 128) return launch(s.fp32 ? return_grad_kernel<float, 128> : return_grad_kernel<uint16_t, 128>, 2);
-  return launch(s.fp32 ? return_grad_kernel<float, 256> : return_grad_kernel<uint16_t, 256>, 1);
+  auto pick = [&](auto v) {
+    using V = decltype(v);
+    if (units <= 32) return launch(return_grad_kernel<V, 32, 1>, return_grad_kernel<V, 32, 4>, 8);
+    if (units <= 64) return launch(return_grad_kernel<V, 64, 1>, return_grad_kernel<V, 64, 4>, 4);
+    if (units <= 128) return launch(return_grad_kernel<V, 128, 1>, return_grad_kernel<V, 128, 4>, 2);
+    return launch(return_grad_kernel<V, 256, 1>, return_grad_kernel<V, 256, 4>, 1);
+  };
+  return s.fp32 ? pick(float{}) : pick(uint16_t{});
 }
 
 }  // namespace moe
