@@ -262,65 +262,60 @@ struct Elems<float> {
   }
 };
 
-// A row position as read from the caller's slot_pos: a routed row in [0, S), or -1 for a dropped
-// slot or (reported) for anything else.  `place` is the row the slot owns, routed or dropped.
-__device__ __forceinline__ int routed_row(int p, int64_t S, int32_t* status) {
-  if (p < 0) return -1;
-  if (p >= S) {
-    if (status) report_device_error(status, kDevBadIndex);
-    return -1;
-  }
-  return p;
-}
+// The row of a slot as read from the caller's slot_pos: -1 for a dropped slot, and for a position
+// past the rows (not sort_tokens's), which nothing may read.
+__device__ __forceinline__ int routed_row(int p, int64_t S) { return p >= 0 && p < S ? p : -1; }
 
 // out[t] = sum_j w[t, j] rows[p] (+ shared[t]); w == NULL: weights 1 (the gradient of the sort).
-// One thread per (token, 16-byte unit); the loads of up to four ranks are issued together.
-template <typename V>
+// A group of threads (threadIdx.y) per token, a thread per 16-byte unit; the loads of kTogether ranks
+// are issued together (four: 32768 x 2048, k = 10 takes 234 us, with two 269, with eight 253, which
+// leave fewer CTAs per SM).
+template <typename V, int kTogether>
 __global__ void __launch_bounds__(kThreads) return_kernel(const uint4* __restrict__ rows,
                                                           const int32_t* __restrict__ slot_pos,
                                                           const float* __restrict__ w, const uint4* __restrict__ shared,
                                                           int64_t T, int units, int k, uint4* __restrict__ out) {
   constexpr int n = Elems<V>::n;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   pdl_wait();
-  if (idx >= T * units) return;
-  const int64_t t = idx / units;
-  const int u = static_cast<int>(idx - t * units);
+  if (t >= T) return;
   const int64_t S = T * k;
-  float acc[n];
+  for (int u = threadIdx.x; u < units; u += blockDim.x) {
+    float acc[n];
 #pragma unroll
-  for (int i = 0; i < n; ++i) acc[i] = 0.0f;
-  for (int j0 = 0; j0 < k; j0 += 4) {
-    uint4 q[4];
-    float wj[4];
-    bool take[4];
+    for (int i = 0; i < n; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < k; j0 += kTogether) {
+      uint4 q[kTogether];
+      float wj[kTogether];
+      bool take[kTogether];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      take[i] = false;
-      if (j0 + i < k) {
-        const int p = routed_row(__ldg(slot_pos + t * k + j0 + i), S, nullptr);
-        take[i] = p >= 0;
-        wj[i] = w ? __ldg(w + t * k + j0 + i) : 1.0f;
-        if (take[i]) q[i] = __ldg(rows + static_cast<int64_t>(p) * units + u);
+      for (int i = 0; i < kTogether; ++i) {
+        take[i] = false;
+        if (j0 + i < k) {
+          const int p = routed_row(__ldg(slot_pos + t * k + j0 + i), S);
+          take[i] = p >= 0;
+          wj[i] = w ? __ldg(w + t * k + j0 + i) : 1.0f;
+          if (take[i]) q[i] = __ldg(rows + static_cast<int64_t>(p) * units + u);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTogether; ++i) {
+        if (take[i]) {
+          float f[n];
+          Elems<V>::get(q[i], f);
+#pragma unroll
+          for (int c = 0; c < n; ++c) acc[c] = fmaf(wj[i], f[c], acc[c]);
+        }
       }
     }
+    if (shared) {
+      float f[n];
+      Elems<V>::get(__ldg(shared + t * units + u), f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (take[i]) {
-        float f[n];
-        Elems<V>::get(q[i], f);
-#pragma unroll
-        for (int c = 0; c < n; ++c) acc[c] = fmaf(wj[i], f[c], acc[c]);
-      }
+      for (int c = 0; c < n; ++c) acc[c] += f[c];
     }
+    out[t * units + u] = Elems<V>::put(acc);
   }
-  if (shared) {
-    float f[n];
-    Elems<V>::get(__ldg(shared + idx), f);
-#pragma unroll
-    for (int c = 0; c < n; ++c) acc[c] += f[c];
-  }
-  out[idx] = Elems<V>::put(acc);
 }
 
 // The gradient of the weighted return, TX threads per token: for each rank the row w dout[t] (zeros
@@ -347,7 +342,7 @@ __global__ void __launch_bounds__(kThreads) return_grad_kernel(const uint4* __re
       for (int i = 0; i < kTogether; ++i) {
         const bool rank = kTogether == 1 || j0 + i < k;
         const int raw = rank ? __ldg(slot_pos + t * k + j0 + i) : 0;
-        p[i] = rank ? routed_row(raw, S, nullptr) : -1;
+        p[i] = rank ? routed_row(raw, S) : -1;
         place[i] = p[i] >= 0 ? p[i] : -1 - raw;   // the zero row of a dropped slot (skipped if it is out of range)
         if (!rank || place[i] >= S) place[i] = -1;
         wj[i] = p[i] >= 0 ? __ldg(w + t * k + j0 + i) : 0.0f;
@@ -438,11 +433,11 @@ cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t*
 cudaError_t launch_return_tokens(const SortShape& s, const void* rows, const int32_t* slot_pos, const float* w,
                                  const void* shared, void* out, cudaStream_t st) {
   const int units = units_of(s);
-  const int64_t blocks = (static_cast<int64_t>(s.T) * units + kThreads - 1) / kThreads;
-  auto kern = s.fp32 ? return_kernel<float> : return_kernel<uint16_t>;
-  return launch_pdl(true, kern, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st,
-                    static_cast<const uint4*>(rows), slot_pos, w, static_cast<const uint4*>(shared),
-                    static_cast<int64_t>(s.T), units, s.k, static_cast<uint4*>(out));
+  const dim3 block = token_block(units);
+  auto kern = s.k <= 2 ? (s.fp32 ? return_kernel<float, 2> : return_kernel<uint16_t, 2>)
+                       : (s.fp32 ? return_kernel<float, 4> : return_kernel<uint16_t, 4>);
+  return launch_pdl(true, kern, dim3((s.T + block.y - 1) / block.y), block, 0, st, static_cast<const uint4*>(rows), slot_pos,
+                    w, static_cast<const uint4*>(shared), static_cast<int64_t>(s.T), units, s.k, static_cast<uint4*>(out));
 }
 
 cudaError_t launch_return_tokens_grad(const SortShape& s, const void* dout, const void* ys, const int32_t* slot_pos,
