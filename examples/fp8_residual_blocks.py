@@ -1,0 +1,160 @@
+"""Two residual blocks around routed e4m3 experts, forward and backward, from the package's operators.
+
+The experts are frozen: their matrices are quantized once, with a scale per 128 x 128 block, and kept
+together with their transposed layout for the backward pass.  The norms, the gates and the routers
+learn.  One training step runs, per block,
+
+    forward   route_topk, sort_tokens, block_fp8_matmul (gate and up), SwiGLU, block_fp8_matmul
+              (down), return_tokens, norm_after (residual update, and the next block's norm)
+    backward  norm_after_backward, return_tokens_backward, block_fp8_matmul on the transposed down
+              matrices, SwiGLU's gradient, block_fp8_matmul on the transposed gate and up matrices,
+              sort_tokens_backward
+
+with norm_before and its gradient at the entry.  The router's small product, SwiGLU and the optimizer
+are plain torch.
+
+    python examples/fp8_residual_blocks.py [--tokens 512] [--steps 20]
+"""
+import argparse
+import os
+import sys
+from dataclasses import dataclass, field
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import quantized_moe_expert_nvfp4_gb300 as moe  # noqa: E402
+
+EPS = 1e-6
+
+
+def swiglu(gu):
+    g, u = gu.float().chunk(2, dim=1)
+    return (torch.nn.functional.silu(g) * u).to(torch.bfloat16)
+
+
+def swiglu_backward(dh, gu):
+    g, u = gu.float().chunk(2, dim=1)
+    s = torch.sigmoid(g)
+    dh = dh.float()
+    return torch.cat([dh * u * s * (1 + g * (1 - s)), dh * g * s], dim=1).to(torch.bfloat16)
+
+
+@dataclass
+class Block:
+    """One block: frozen experts, and what learns."""
+    shape: moe.Shape
+    gate_up: moe.BlockFP8Weights          # [E, 2 I, H]
+    down: moe.BlockFP8Weights             # [E, H, I]
+    router: torch.Tensor                  # fp32 [E, H]
+    w_in: torch.Tensor                    # fp32 [H]: norm before the block
+    w_out: torch.Tensor                   # fp32 [H]: norm after it
+    gate: torch.Tensor                    # fp32 [H]
+    saved: dict = field(default_factory=dict)
+
+    def __post_init__(self):
+        s = self.shape
+        self.gate_up_t, self.down_t = moe.transpose_block_fp8(self.gate_up), moe.transpose_block_fp8(self.down)
+        self.ws_sort = moe.sort_workspace(s.T, s.E, s.k)
+        widest = self.gate_up_t if 2 * s.I > s.H else self.gate_up
+        self.ws_product = moe.block_fp8_workspace(s.S, widest)
+        self.ws_norm = moe.norm_workspace(s.T, s.H)
+
+    def experts(self, n, padding):
+        """The routed experts on normed rows n [T, H]; tokens under `padding` go to none."""
+        s = self.shape
+        ids, w = moe.route_topk(n.float() @ self.router.t(), s)
+        ids = torch.where(padding[:, None], -1, ids)
+        xs, offsets, _, pos = moe.sort_tokens(n, ids, s.E, self.ws_sort)
+        gu = moe.block_fp8_matmul(xs, self.gate_up, self.ws_product, offsets=offsets)
+        ys = moe.block_fp8_matmul(swiglu(gu), self.down, self.ws_product, offsets=offsets)
+        self.saved = dict(n=n, ids=ids, w=w, offsets=offsets, pos=pos, gu=gu, ys=ys)
+        return moe.return_tokens(ys, pos, w)
+
+    def experts_backward(self, dy, grads):
+        """dn, with the router's gradient put into grads."""
+        v, s = self.saved, self.shape
+        dys, dw = moe.return_tokens_backward(dy, v["ys"], v["pos"], v["w"])
+        dh = moe.block_fp8_matmul(dys, self.down_t, self.ws_product, offsets=v["offsets"])
+        dgu = swiglu_backward(dh, v["gu"])
+        dxs = moe.block_fp8_matmul(dgu, self.gate_up_t, self.ws_product, offsets=v["offsets"])
+        dn = moe.sort_tokens_backward(dxs, v["pos"])
+        # weights are a softmax over the picked logits
+        dz = v["w"] * (dw - (v["w"] * dw).sum(1, keepdim=True))
+        dlogits = torch.zeros(s.T, s.E, device=dy.device).scatter_add_(1, v["ids"].long().clamp_min(0), dz)
+        grads["router"] = dlogits.t() @ v["n"].float()
+        return (dn.float() + dlogits @ self.router).to(torch.bfloat16)
+
+
+def forward(blocks, x, padding):
+    n, rstd = moe.norm_before(x, blocks[0].w_in, eps=EPS)
+    trace = [(x, rstd)]
+    for i, b in enumerate(blocks):
+        y = b.experts(n, padding)
+        w_next = blocks[i + 1].w_in if i + 1 < len(blocks) else None
+        x, n, r_y, r_out = moe.norm_after(y, x, b.w_out, gate=b.gate, w_next=w_next, eps=EPS)
+        trace.append((x, r_out, y, r_y))
+    return x, trace
+
+
+def backward(blocks, trace, dout):
+    """Gradients of every block's parameters (a dict per block) and of the input."""
+    grads = [{} for _ in blocks]
+    dn = None
+    for i in range(len(blocks) - 1, -1, -1):
+        b, (out, r_out, y, r_y) = blocks[i], trace[i + 1]
+        more = {} if dn is None else dict(dn=dn, out=out, w_next=blocks[i + 1].w_in, rstd_next=r_out)
+        dy, dx, grads[i]["w_out"], grads[i]["gate"], dw_next = moe.norm_after_backward(dout, y, b.w_out, r_y, b.ws_norm,
+                                                                                       gate=b.gate, **more)
+        if dn is not None:
+            grads[i + 1]["w_in"] = dw_next
+        dn, dout = b.experts_backward(dy, grads[i]), dx
+    x, rstd = trace[0]
+    dx, grads[0]["w_in"] = moe.norm_before_backward(dn, x, blocks[0].w_in, rstd, blocks[0].ws_norm, dresidual=dout)
+    return grads, dx
+
+
+def make_blocks(count, T, H, inner, E, k, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    r = lambda *s, scale=1.0: torch.randn(*s, generator=g, device="cuda") * scale  # noqa: E731
+    return [Block(moe.Shape(T=T, H=H, I=inner, E=E, k=k, has_shared=0), moe.quantize_block_fp8(r(E, 2 * inner, H, scale=H ** -0.5)),
+                  moe.quantize_block_fp8(r(E, H, inner, scale=inner ** -0.5)), r(E, H, scale=H ** -0.5), 1 + r(H, scale=0.05),
+                  1 + r(H, scale=0.05), 0.5 + r(H, scale=0.05)) for _ in range(count)]
+
+
+def train(blocks, x, target, padding, steps, lr=0.2):
+    """Steps of gradient descent on the mean squared error; returns the losses.  The error is a mean over
+    the H columns, so a column's parameter takes steps of lr H; the routers, whose picks move, of less."""
+    losses = []
+    for _ in range(steps):
+        out, trace = forward(blocks, x, padding)
+        diff = out.float() - target
+        losses.append(diff.square().mean())
+        grads, _ = backward(blocks, trace, (2 / diff.numel() * diff).to(x.dtype))
+        for b, grad in zip(blocks, grads):
+            for name, value in grad.items():
+                getattr(b, name).sub_(lr * x.shape[1] * (0.01 if name == "router" else 1.0) * value)
+    return [float(v) for v in losses]
+
+
+def main():
+    p = argparse.ArgumentParser(description=__doc__.splitlines()[0])
+    p.add_argument("--tokens", type=int, default=512)
+    p.add_argument("--steps", type=int, default=20)
+    a = p.parse_args()
+    T, H = a.tokens, 512
+    blocks = make_blocks(2, T, H, inner=256, E=32, k=4)
+    teacher = make_blocks(2, T, H, inner=256, E=32, k=4)
+    for b in teacher:
+        b.gate.mul_(0.5).add_(0.5)
+        b.w_out.mul_(1.2)
+    x = torch.randn(T, H, device="cuda")
+    padding = torch.arange(T, device="cuda") >= T - T // 16
+    target = forward(teacher, x, padding)[0].float()
+    losses = train(blocks, x, target, padding, a.steps)
+    print(f"loss {losses[0]:.5f} -> {losses[-1]:.5f} in {a.steps} steps")
+
+
+if __name__ == "__main__":
+    main()
