@@ -292,7 +292,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_before_grad_kernel(NormAr
 // so the three row sums e oh, u v and oh v are taken together.  A token's gate has the gradient
 // sum(d v); an element's b w' d yh.  The column sum q = sum_t d yh (times a token's or an
 // element's gate) is the branch weight's gradient over b g, and a channel gate's over b w'.
-template <typename R, typename Y, int U, int kMaxThreads, bool kNext>
+// kKeep: the vectors of the columns stay in registers and rows are loaded ahead; above 4096 columns
+// (two units per thread) there are no registers for either (4096 x 5120: 104 instead of 112 us).
+template <typename R, typename Y, int U, int kMaxThreads, bool kKeep, bool kNext>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArgs a) {
   __shared__ Vec8 s_cols[kGradThreads];
   Vec8 q_col[U], dwn[U], bw[U], wn[U];    // bw: b w' times a channel's gate
@@ -316,18 +318,22 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArg
     if (kNext) q_rn = __ldg(a.rstd_next_in + t);
   };
   pdl_wait();
-  if (at.row < a.T) load_row(at.row);
-  EACH_UNIT(i) {
+  if (kKeep && at.row < a.T) load_row(at.row);
+  auto load_bw = [&](int i) {
     bw[i] = gated_weight(a, UNIT(i));
-    if (kNext) wn[i] = load_vec(a.w_next, UNIT(i), a.w_off);
+    EACH(c) bw[i].p[c] = mul2(bw[i].p[c], both(a.b));
+  };
+  EACH_UNIT(i) {
+    if (kKeep) load_bw(i);
+    if (kKeep && kNext) wn[i] = load_vec(a.w_next, UNIT(i), a.w_off);
     EACH(c) {
-      bw[i].p[c] = mul2(bw[i].p[c], both(a.b));
       q_col[i].p[c] = 0;
       dwn[i].p[c] = 0;
     }
   }
   const bool by_element = a.gate_kind == MOE_GATE_ELEMENT;
   for (int64_t t = at.row; t < a.T; t += at.stride) {
+    if (!kKeep) load_row(t);
     const float rstd = q_rstd, rn = q_rn;
     Vec8 d[U], yh[U], oh[U];
     f32x2 s_eo = 0, s_uv = 0, s_ov = 0;
@@ -335,6 +341,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArg
       d[i] = qd[i].get();
       yh[i] = qy[i].get();
       EACH(c) yh[i].p[c] = mul2(yh[i].p[c], both(rstd));
+      if (!kKeep) load_bw(i);
       Vec8 v;
       EACH(c) v.p[c] = mul2(yh[i].p[c], bw[i].p[c]);
       if (by_element) {
@@ -343,6 +350,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArg
       }
       if (kNext) {
         oh[i] = qo[i].get();
+        if (!kKeep) wn[i] = load_vec(a.w_next, UNIT(i), a.w_off);
         Vec8 e = qn[i].get();
         EACH(c) {
           oh[i].p[c] = mul2(oh[i].p[c], both(rn));
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArg
       }
       EACH(c) s_uv = fma2(d[i].p[c], v.p[c], s_uv);
     }
-    if (t + at.stride < a.T) load_row(t + at.stride);
+    if (kKeep && t + at.stride < a.T) load_row(t + at.stride);
     float dv, back = 0.0f;
     if (kNext) {
       float sums[3] = {sum2(s_eo), sum2(s_uv), sum2(s_ov)};
@@ -372,6 +380,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArg
     const f32x2 m = both(-rstd * gt * (dv * a.inv_h)), rg = both(rstd * gt);
     EACH_UNIT(i) {
       const int64_t u = t * a.units + UNIT(i);
+      if (!kKeep) load_bw(i);
       if (kNext) EACH(c) d[i].p[c] = fma2(oh[i].p[c], both(back), d[i].p[c]);
       Vec8 r;
       EACH(c) r.p[c] = mul2(d[i].p[c], both(a.a));
@@ -461,7 +470,11 @@ NormLaunch launch_of(int64_t T, int units, int one_unit, int threads, int per_sm
   l.grid = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min((T + y - 1) / y, most))));
   return l;
 }
-NormLaunch forward_launch(int64_t T, int units, int n_sm) { return launch_of(T, units, 32, kForwardThreads, 2, n_sm); }
+// CTAs of kForwardThreads per SM: registers allow four of `before` (two: 32768 x 2048 in 52 instead
+// of 43 us) and two of `after`.
+NormLaunch forward_launch(int64_t T, int units, int per_sm, int n_sm) {
+  return launch_of(T, units, 32, kForwardThreads, per_sm, n_sm);
+}
 NormLaunch grad_launch(int64_t T, int units, int n_sm) {
   return launch_of(T, units, kOneUnit, kGradThreads, 1, std::min(n_sm, kMaxSms));
 }
@@ -479,15 +492,16 @@ NormArgs args_of(const moe_norm_t& s) {
   return a;
 }
 
-// Launch bounds of 256 or 512 threads leave 128 registers, those of 1024 (above 8192 columns) 64,
-// some of them spilled.
+// Launch bounds of 256 x 2 or 512 threads leave 128 registers, those of 256 x 4 or 1024 (above 8192
+// columns) 64, some of them spilled in the latter.
 #define PICK_FORWARD(one, two, wide, more) (s.H / 8 <= 32 ? one : s.H / 8 <= 512 ? two : s.H / 8 <= 1024 ? wide : more)
 #define PICK_GRADIENT(one, two, more) (s.H / 8 <= kOneUnit ? one : s.H / 8 <= 2 * kOneUnit ? two : more)
-#define PICK_BEFORE(K, R) PICK_FORWARD((K<R, 1, 256, 2>), (K<R, 2, 256, 2>), (K<R, 2, 512, 1>), (K<R, 2, 1024, 1>))
+#define PICK_BEFORE(K, R) PICK_FORWARD((K<R, 1, 256, 4>), (K<R, 2, 256, 4>), (K<R, 2, 512, 2>), (K<R, 2, 1024, 1>))
 #define PICK_GRAD(K, R) PICK_GRADIENT((K<R, 1, 512>), (K<R, 2, 512>), (K<R, 2, 1024>))
 #define PICK_AFTER(K, R, Y, next) \
   PICK_FORWARD((K<R, Y, 1, 256, 2, next>), (K<R, Y, 2, 256, 2, next>), (K<R, Y, 2, 512, 1, next>), (K<R, Y, 2, 1024, 1, next>))
-#define PICK_AFTER_GRAD(K, R, Y, next) PICK_GRADIENT((K<R, Y, 1, 512, next>), (K<R, Y, 2, 512, next>), (K<R, Y, 2, 1024, next>))
+#define PICK_AFTER_GRAD(K, R, Y, next) \
+  PICK_GRADIENT((K<R, Y, 1, 512, true, next>), (K<R, Y, 2, 512, false, next>), (K<R, Y, 2, 1024, false, next>))
 #define PICK_NEXT(PICK, K, R, Y) (next ? PICK(K, R, Y, true) : PICK(K, R, Y, false))
 #define PICK_TYPES(PICK, K)                                                                                          \
   (s.residual_fp32 ? (s.branch_fp32 ? PICK_NEXT(PICK, K, float, float) : PICK_NEXT(PICK, K, float, uint16_t))        \
@@ -508,7 +522,7 @@ cudaError_t launch_norm_before(const moe_norm_t& s, const void* x, const float* 
   a.n = n;
   a.rstd = rstd;
   auto kern = s.residual_fp32 ? PICK_BEFORE(norm_before_kernel, float) : PICK_BEFORE(norm_before_kernel, uint16_t);
-  const NormLaunch l = forward_launch(s.T, a.units, n_sm);
+  const NormLaunch l = forward_launch(s.T, a.units, 4, n_sm);
   return launch_pdl(true, kern, l.grid, l.block, 0, st, a);
 }
 
@@ -529,7 +543,7 @@ cudaError_t launch_norm_after(const moe_norm_t& s, const void* y, const void* x,
   a.rstd_next = rstd_next;
   const bool next = w_next != nullptr;
   auto kern = PICK_TYPES(PICK_AFTER, norm_after_kernel);
-  const NormLaunch l = forward_launch(s.T, a.units, n_sm);
+  const NormLaunch l = forward_launch(s.T, a.units, 2, n_sm);
   return launch_pdl(true, kern, l.grid, l.block, 0, st, a);
 }
 
