@@ -209,18 +209,19 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_after_kernel(NormArg
 // Adds the groups' column sums in group order (through shared memory) and writes the CTA's row.
 template <int U>
 __device__ __forceinline__ void write_part(const NormArgs& a, int which, Vec8 (&s)[U], Vec8* s_cols) {
-  if (blockDim.y > 1) {                 // one unit per thread then
-    __syncthreads();
-    if (threadIdx.y > 0) s_cols[(threadIdx.y - 1) * blockDim.x + threadIdx.x] = s[0];
-    __syncthreads();
-  }
-  if (threadIdx.y > 0) return;
-  for (int g = 1; g < static_cast<int>(blockDim.y); ++g) {
-    const Vec8 o = s_cols[(g - 1) * blockDim.x + threadIdx.x];
-    EACH(c) s[0].p[c] = add2(s[0].p[c], o.p[c]);
-  }
   float* row = a.part + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.units * 8;
-  EACH_UNIT(i) {
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    if (blockDim.y > 1) {
+      __syncthreads();
+      if (threadIdx.y > 0) s_cols[(threadIdx.y - 1) * blockDim.x + threadIdx.x] = s[i];
+      __syncthreads();
+    }
+    if (threadIdx.y > 0 || UNIT(i) >= a.units) continue;
+    for (int g = 1; g < static_cast<int>(blockDim.y); ++g) {
+      const Vec8 o = s_cols[(g - 1) * blockDim.x + threadIdx.x];
+      EACH(c) s[i].p[c] = add2(s[i].p[c], o.p[c]);
+    }
     Unit8<float> q;
     q.set(s[i]);
     q.store(row, UNIT(i));
@@ -444,11 +445,12 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const float* __restri
   }
 }
 
-// Units per thread: gradients one for rows of up to kOneUnit units, else two; forward one up to 32
-// units, else two: a row's sums cost a thread about as many instructions as a unit's arithmetic, and
-// the forward kernels are bound by their instructions (32768 x 2048 with the next norm: 115 us with
-// one and 87 us with two).
-constexpr int kOneUnit = 512;
+// Units per thread: one for rows of up to this many units, else two.  A row's sums cost a thread
+// about as many instructions as a unit's arithmetic, and the kernels are bound by their instructions
+// and latencies before HBM: `after` with the next norm of 32768 x 2048 takes 115 us with one unit and
+// 87 us with two, the gradient of `before` of 16384 x 2048 56 and 47 us (2999 x 1000: 11 and 15 us).
+// The gradient of `after` has no registers for a second unit below 4096 columns.
+constexpr int kForwardOneUnit = 32, kBeforeGradOneUnit = 128, kOneUnit = 512;
 constexpr int kForwardThreads = 256;
 constexpr int kMaxSms = 160;     // the workspace holds the column sums of this many CTAs
 
@@ -463,7 +465,8 @@ struct NormLaunch {
   dim3 grid, block;
 };
 NormLaunch launch_of(int64_t T, int units, int one_unit, int threads, int per_sm, int n_sm) {
-  const int x = row_threads(units, one_unit), y = std::max(1, threads / x);
+  const int x = row_threads(units, one_unit);
+  const int y = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(threads / x, T / n_sm)));   // few rows: on all SMs
   const int64_t most = static_cast<int64_t>(n_sm) * std::max(1, per_sm * threads / (x * y));
   NormLaunch l;
   l.block = dim3(x, y);
@@ -473,10 +476,10 @@ NormLaunch launch_of(int64_t T, int units, int one_unit, int threads, int per_sm
 // CTAs of kForwardThreads per SM: registers allow four of `before` (two: 32768 x 2048 in 52 instead
 // of 43 us) and two of `after`.
 NormLaunch forward_launch(int64_t T, int units, int per_sm, int n_sm) {
-  return launch_of(T, units, 32, kForwardThreads, per_sm, n_sm);
+  return launch_of(T, units, kForwardOneUnit, kForwardThreads, per_sm, n_sm);
 }
-NormLaunch grad_launch(int64_t T, int units, int n_sm) {
-  return launch_of(T, units, kOneUnit, kGradThreads, 1, std::min(n_sm, kMaxSms));
+NormLaunch grad_launch(int64_t T, int units, int one_unit, int n_sm) {
+  return launch_of(T, units, one_unit, kGradThreads, 1, std::min(n_sm, kMaxSms));
 }
 
 NormArgs args_of(const moe_norm_t& s) {
@@ -494,10 +497,10 @@ NormArgs args_of(const moe_norm_t& s) {
 
 // Launch bounds of 256 x 2 or 512 threads leave 128 registers, those of 256 x 4 or 1024 (above 8192
 // columns) 64, some of them spilled in the latter.
-#define PICK_FORWARD(one, two, wide, more) (s.H / 8 <= 32 ? one : s.H / 8 <= 512 ? two : s.H / 8 <= 1024 ? wide : more)
+#define PICK_FORWARD(one, two, wide, more) (s.H / 8 <= kForwardOneUnit ? one : s.H / 8 <= 512 ? two : s.H / 8 <= 1024 ? wide : more)
 #define PICK_GRADIENT(one, two, more) (s.H / 8 <= kOneUnit ? one : s.H / 8 <= 2 * kOneUnit ? two : more)
 #define PICK_BEFORE(K, R) PICK_FORWARD((K<R, 1, 256, 4>), (K<R, 2, 256, 4>), (K<R, 2, 512, 2>), (K<R, 2, 1024, 1>))
-#define PICK_GRAD(K, R) PICK_GRADIENT((K<R, 1, 512>), (K<R, 2, 512>), (K<R, 2, 1024>))
+#define PICK_GRAD(K, R) (s.H / 8 <= kBeforeGradOneUnit ? K<R, 1, 512> : s.H / 8 <= 2 * kOneUnit ? K<R, 2, 512> : K<R, 2, 1024>)
 #define PICK_AFTER(K, R, Y, next) \
   PICK_FORWARD((K<R, Y, 1, 256, 2, next>), (K<R, Y, 2, 256, 2, next>), (K<R, Y, 2, 512, 1, next>), (K<R, Y, 2, 1024, 1, next>))
 #define PICK_AFTER_GRAD(K, R, Y, next) \
@@ -510,7 +513,9 @@ NormArgs args_of(const moe_norm_t& s) {
 }  // namespace
 
 // CTAs that write column sums, at most (the size of the workspace).
-int64_t norm_max_parts(int64_t T, int H) { return grad_launch(T, H / 8, kMaxSms).grid.x; }
+int64_t norm_max_parts(int64_t T, int H) {
+  return std::max(grad_launch(T, H / 8, kBeforeGradOneUnit, kMaxSms).grid.x, grad_launch(T, H / 8, kOneUnit, kMaxSms).grid.x);
+}
 
 cudaError_t launch_norm_before(const moe_norm_t& s, const void* x, const float* w, void* n, float* rstd, cudaStream_t st) {
   int n_sm = 0;
@@ -560,7 +565,7 @@ cudaError_t launch_norm_before_grad(const moe_norm_t& s, const void* dn, const v
   a.dres = dres;
   a.dx = dx;
   a.part = part;
-  const NormLaunch l = grad_launch(s.T, a.units, n_sm);
+  const NormLaunch l = grad_launch(s.T, a.units, kBeforeGradOneUnit, n_sm);
   const int grid = static_cast<int>(l.grid.x);
   auto kern = s.residual_fp32 ? PICK_GRAD(norm_before_grad_kernel, float) : PICK_GRAD(norm_before_grad_kernel, uint16_t);
   e = launch_pdl(true, kern, l.grid, l.block, 0, st, a);
@@ -591,7 +596,7 @@ cudaError_t launch_norm_after_grad(const moe_norm_t& s, const void* dout, const 
   a.dx = dx;
   a.dgate = dgate;
   a.part = part;
-  const NormLaunch l = grad_launch(s.T, a.units, n_sm);
+  const NormLaunch l = grad_launch(s.T, a.units, kOneUnit, n_sm);
   const int grid = static_cast<int>(l.grid.x);
   const bool next = w_next != nullptr;
   auto kern = PICK_TYPES(PICK_AFTER_GRAD, norm_after_grad_kernel);
