@@ -7,7 +7,7 @@
 // Every step is one IEEE operation, so the codes are reproducible bit for bit.
 #include <algorithm>
 
-#include "internal.cuh"
+#include "row_units.cuh"
 
 namespace moe {
 namespace {
@@ -26,10 +26,25 @@ __device__ __forceinline__ uint32_t codes2(float a, float b, float inv) {
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3));
 }
 
-// One warp per row and 1024 columns: 8 lanes hold a block (16 bf16 each), so every lane has its four
-// 16-byte loads in flight at once.  codes [rows, 128 KB], zero from K on; scales [rows, KB rounded
-// up to 4], zero from KB on (KB = blocks of a row).
-constexpr int kRowSteps = 2, kRowBlocks = 4 * kRowSteps;
+// A bf16 pair times inv -> two e4m3 codes, the first in the low byte.
+__device__ __forceinline__ uint16_t codes2(uint32_t pair, f32x2 inv) {
+  const float2 q = unpack2(mul2(pack2(__uint_as_float(pair << 16), __uint_as_float(pair & 0xffff0000u)), inv));
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(q.y), "f"(q.x));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, f32x2 inv) {
+  uint32_t r;
+  asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(codes2(a, inv)), "h"(codes2(b, inv)));
+  return r;
+}
+
+// One warp per row and 1024 columns, 8 lanes per block (16 bf16 each) and two blocks per lane, whose
+// four 16-byte loads are in flight at once.  codes [rows, 128 KB], zero from K on; scales [rows, KB
+// rounded up to 4], zero from KB on (KB = blocks of a row).  Bound by its instructions as much as by
+// HBM, so the two blocks' maxima are reduced together, and their four divisions (inverse and scale of
+// each) are one division in four lanes.
+constexpr int kRowBlocks = 8;
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restrict__ x, int64_t rows, int K, int KB,
                                                             int tasks, uint4* __restrict__ codes,
                                                             float* __restrict__ scales) {
@@ -38,12 +53,13 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
   pdl_wait_then_release();   // the product's launch starts with this grid's last wave
   const int64_t r = i / tasks;
   if (r >= rows) return;
-  const int kb0 = static_cast<int>(i - r * tasks) * kRowBlocks;
+  const int kb0 = static_cast<int>(i - r * tasks) * kRowBlocks + (lane >> 3);   // this lane's blocks: kb0, kb0 + 4
   const int units = K / 16, pitch = (KB + 3) & ~3;
-  uint4 q[kRowSteps][2];
+  uint4 q[2][2];
+  __nv_bfloat162 m[2];
 #pragma unroll
-  for (int s = 0; s < kRowSteps; ++s) {
-    const int u = kb0 * 8 + s * 32 + lane;
+  for (int s = 0; s < 2; ++s) {
+    const int u = (kb0 + 4 * s) * 8 + (lane & 7);
     q[s][0] = q[s][1] = make_uint4(0, 0, 0, 0);
     if (u < units) {
       q[s][0] = __ldg(x + (r * units + u) * 2);
@@ -51,23 +67,30 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
     }
   }
 #pragma unroll
-  for (int s = 0; s < kRowSteps; ++s) {
+  for (int s = 0; s < 2; ++s) {
     const uint32_t w[8] = {q[s][0].x, q[s][0].y, q[s][0].z, q[s][0].w, q[s][1].x, q[s][1].y, q[s][1].z, q[s][1].w};
-    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+    m[s] = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
 #pragma unroll
-    for (int c = 1; c < 8; ++c) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[c])));
+    for (int c = 1; c < 8; ++c) m[s] = __hmax2_nan(m[s], __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[c])));
+  }
+  // the two blocks' maxima side by side
+  __nv_bfloat162 top = __hmax2_nan(__lows2bfloat162(m[0], m[1]), __highs2bfloat162(m[0], m[1]));
 #pragma unroll
-    for (int d = 4; d > 0; d >>= 1) m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float inv, scale;
-    block_rule(max_nan(__low2float(m), __high2float(m)), inv, scale);
-    uint32_t o[4];
+  for (int d = 4; d > 0; d >>= 1) top = __hmax2_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+  // lanes 0..3 of each four: inverse and scale of the first block, inverse and scale of the second
+  const float amax = (lane & 2) ? __high2float(top) : __low2float(top);
+  const bool usable = amax > 0.0f && amax <= 3.402823466e38f;
+  const float of = usable ? ((lane & 1) ? amax : 448.0f) : 1.0f, by = usable ? ((lane & 1) ? 448.0f : amax) : 1.0f;
+  const float ratio = __fdiv_rn(of, by);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      o[c] = codes2(__uint_as_float(w[2 * c] << 16), __uint_as_float(w[2 * c] & 0xffff0000u), inv) |
-             (codes2(__uint_as_float(w[2 * c + 1] << 16), __uint_as_float(w[2 * c + 1] & 0xffff0000u), inv) << 16);
-    const int kb = kb0 + s * 4 + (lane >> 3);
-    if (kb < KB) codes[r * KB * 8 + kb * 8 + (lane & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
-    if ((lane & 7) == 0 && kb < pitch) scales[r * pitch + kb] = kb < KB ? scale : 0.0f;
+  for (int s = 0; s < 2; ++s) {
+    const f32x2 inv = both(__shfl_sync(0xffffffffu, ratio, (lane & ~3) + 2 * s));
+    const int kb = kb0 + 4 * s;
+    if (kb < KB)
+      codes[r * KB * 8 + kb * 8 + (lane & 7)] =
+          make_uint4(codes4(q[s][0].x, q[s][0].y, inv), codes4(q[s][0].z, q[s][0].w, inv),
+                     codes4(q[s][1].x, q[s][1].y, inv), codes4(q[s][1].z, q[s][1].w, inv));
+    if ((lane & 7) == 2 * s + 1 && kb < pitch) scales[r * pitch + kb] = kb < KB ? ratio : 0.0f;
   }
 }
 
