@@ -182,8 +182,9 @@ moe_status_t moe_block_fp8_matmul(const uint16_t* x, int64_t M, const int32_t* o
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   char* b = static_cast<char*>(ws);
   BlockFp8Args a;
-  a.x_codes = reinterpret_cast<const uint8_t*>(b + L.codes);
-  a.x_scales = reinterpret_cast<const float*>(b + L.scales);
+  a.x = x;
+  a.x_codes = reinterpret_cast<uint8_t*>(b + L.codes);
+  a.x_scales = reinterpret_cast<float*>(b + L.scales);
   a.w_codes = w->codes;
   a.w_scales = w->scales;
   a.offsets = offsets;
@@ -194,10 +195,7 @@ moe_status_t moe_block_fp8_matmul(const uint16_t* x, int64_t M, const int32_t* o
   a.out = out;
   a.out_fp32 = out_is_fp32 != 0;
   a.status = reinterpret_cast<int32_t*>(b);
-  cudaError_t e = launch_quantize_rows_block(x, M, w->K, reinterpret_cast<uint8_t*>(b + L.codes),
-                                             reinterpret_cast<float*>(b + L.scales), cs);
-  if (e == cudaSuccess) e = launch_block_fp8_matmul(a, cs);
-  return cuda_status(e);
+  return cuda_status(launch_block_fp8_matmul(a, cs));
 }
 
 size_t moe_norm_workspace_size(int32_t T, int32_t H) {

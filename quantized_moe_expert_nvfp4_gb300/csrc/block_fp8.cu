@@ -7,7 +7,7 @@
 // Every step is one IEEE operation, so the codes are reproducible bit for bit.
 #include <algorithm>
 
-#include "row_units.cuh"
+#include "quantize_block.cuh"
 
 namespace moe {
 namespace {
@@ -24,19 +24,6 @@ __device__ __forceinline__ float max_nan(float a, float b) { return a != a ? a :
 __device__ __forceinline__ uint32_t codes2(float a, float b, float inv) {
   const float2 q = make_float2(__fmul_rn(a, inv), __fmul_rn(b, inv));
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3));
-}
-
-// A bf16 pair times inv -> two e4m3 codes, the first in the low byte.
-__device__ __forceinline__ uint16_t codes2(uint32_t pair, f32x2 inv) {
-  const float2 q = unpack2(mul2(pack2(__uint_as_float(pair << 16), __uint_as_float(pair & 0xffff0000u)), inv));
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(q.y), "f"(q.x));
-  return r;
-}
-__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, f32x2 inv) {
-  uint32_t r;
-  asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(codes2(a, inv)), "h"(codes2(b, inv)));
-  return r;
 }
 
 // One warp per row and 1024 columns, 8 lanes per block (16 bf16 each) and two blocks per lane, whose
@@ -66,30 +53,19 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const uint4* __restr
       q[s][1] = __ldg(x + (r * units + u) * 2 + 1);
     }
   }
-#pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const uint32_t w[8] = {q[s][0].x, q[s][0].y, q[s][0].z, q[s][0].w, q[s][1].x, q[s][1].y, q[s][1].z, q[s][1].w};
-    m[s] = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
-#pragma unroll
-    for (int c = 1; c < 8; ++c) m[s] = __hmax2_nan(m[s], __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[c])));
-  }
+  m[0] = max16(q[0]);
+  m[1] = max16(q[1]);
   // the two blocks' maxima side by side
   __nv_bfloat162 top = __hmax2_nan(__lows2bfloat162(m[0], m[1]), __highs2bfloat162(m[0], m[1]));
 #pragma unroll
   for (int d = 4; d > 0; d >>= 1) top = __hmax2_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
   // lanes 0..3 of each four: inverse and scale of the first block, inverse and scale of the second
-  const float amax = (lane & 2) ? __high2float(top) : __low2float(top);
-  const bool usable = amax > 0.0f && amax <= 3.402823466e38f;
-  const float of = usable ? ((lane & 1) ? amax : 448.0f) : 1.0f, by = usable ? ((lane & 1) ? 448.0f : amax) : 1.0f;
-  const float ratio = __fdiv_rn(of, by);
+  const float ratio = block_ratio((lane & 2) ? __high2float(top) : __low2float(top), lane & 1);
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const f32x2 inv = both(__shfl_sync(0xffffffffu, ratio, (lane & ~3) + 2 * s));
     const int kb = kb0 + 4 * s;
-    if (kb < KB)
-      codes[r * KB * 8 + kb * 8 + (lane & 7)] =
-          make_uint4(codes4(q[s][0].x, q[s][0].y, inv), codes4(q[s][0].z, q[s][0].w, inv),
-                     codes4(q[s][1].x, q[s][1].y, inv), codes4(q[s][1].z, q[s][1].w, inv));
+    if (kb < KB) codes[r * KB * 8 + kb * 8 + (lane & 7)] = codes16(q[s], inv);
     if ((lane & 7) == 2 * s + 1 && kb < pitch) scales[r * pitch + kb] = kb < KB ? ratio : 0.0f;
   }
 }

@@ -20,7 +20,7 @@
 #include <algorithm>
 
 #include "group_tiles.cuh"
-#include "internal.cuh"
+#include "quantize_block.cuh"
 #include "tc_common.cuh"
 #include "tensor_map.cuh"
 
@@ -32,30 +32,46 @@ using namespace tc;
 constexpr int kPromoteWgs = 2;                // promoting warpgroups
 constexpr int kThreads = 128 + 128 * kPromoteWgs;
 constexpr int kWarpTmaB = 0, kWarpMma = 1, kWarpTmaA = 2, kWarpAlloc = 3, kWarpPromote = 4;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 12;
+constexpr int kScaleRing = 32;                 // kFused: blocks whose row scales are kept
 constexpr int kChunk = 128;                    // K of a scale block: one 128-byte swizzled row
 constexpr uint32_t kSpinLimit = 1u << 24;      // drain loops only
 constexpr uint64_t kWaitTimeoutNs = 1000000000ull;
 
 constexpr int kRows = 128;                     // rows of a tile that a CTA holds (its TMEM lanes)
 
-// BN: columns of a tile (MMA N).  kPair: a cluster of two CTAs takes a tile of 256 rows with one
-// cta_group::2 MMA; each holds its own rows, half of the matrix tile, and the accumulator of its rows.
-template <int BN, bool kPair>
+// How a CTA comes by its rows.
+enum Mode {
+  kSingle,   // codes from the row quantizer's launch, 128 rows per tile
+  kPair,     // a cluster of two CTAs takes 256 rows with one cta_group::2 MMA; each holds its own rows,
+             // half of the matrix tile, and the accumulator of its rows
+  kFused     // few rows (32 per tile): warps of the CTA quantize them on the way into shared memory
+};
+
+// BN: columns of a tile (MMA N).
+template <int BN, Mode kMode>
 struct Tile {
-  static constexpr int kTileRows = kPair ? 2 * kRows : kRows;
-  static constexpr int kBRows = kPair ? BN / 2 : BN;           // matrix rows in this CTA's shared memory
-  static constexpr int kAStage = kRows * kChunk;               // a stage is one scale block of K
+  static constexpr bool kTwo = kMode == kPair;
+  static constexpr int kTileRows = kTwo ? 2 * kRows : kMode == kFused ? 32 : kRows;
+  static constexpr int kARows = std::min(kTileRows, kRows);    // rows in this CTA's shared memory
+  static constexpr int kBRows = kTwo ? BN / 2 : BN;            // matrix rows in it
+  static constexpr int kAStage = kARows * kChunk;              // a stage is one scale block of K
   static constexpr int kBStage = kBRows * kChunk;
   static constexpr int kBufs = std::min(4, 512 / BN);          // TMEM accumulators
   static constexpr int kTmemCols = kBufs * BN;
-  static constexpr int kCols = BN / kPromoteWgs;               // columns per promoting thread
-  static constexpr int kBoxes = kRows / 16;
-  static constexpr int kWarps = 4 * kPromoteWgs;               // promoting warps
+  static constexpr int kCols = std::max(64, BN / kPromoteWgs);          // columns per promoting thread
+  static constexpr int kBoxes = kMode == kFused ? 1 : kRows / 16;
+  static constexpr int kWarps = BN / kCols * (kARows / 32);    // promoting warps
   static constexpr int kBoxesOut = kCols / 64;                 // staged boxes of 32 rows x 128 bytes per warp
   static constexpr int kStaging = kWarps * kBoxesOut * 4096;
   static constexpr int kStages = std::min(kMaxStages, (220160 - kStaging) / (kAStage + kBStage));
   static constexpr int kSmem = 1024 + kStages * (kAStage + kBStage) + kStaging;
+  // kFused: warps that quantize rows, every kQuantizers-th block of K each.  A warp that waits for the
+  // stage of block i has seen block i - kQuantizers - kStages consumed, and its wait by parity needs
+  // block i - 2 kStages consumed, so there are no more warps than stages.  Row scales are kept for
+  // longer than the stages and accumulators by which the warps run ahead.
+  static constexpr int kQuantizers = std::min(6, kStages);
+  static_assert(kQuantizers <= kStages && kScaleRing > kStages + kBufs + 1, "rings of the quantizing warps");
 };
 
 template <int kBoxes>
@@ -67,17 +83,18 @@ struct Maps {
 };
 
 struct Bars {
-  uint64_t full[kMaxStages], empty[kMaxStages];   // stage: two arrivals (matrix and rows), one commit
+  uint64_t full[kMaxStages], empty[kMaxStages];   // stage: arrivals of matrix and rows; one commit
   uint64_t acc_full[4], acc_empty[4];
+  uint64_t scales[kScaleRing];          // kFused: the row scales of a block are written
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
 };
 
 // Loads of a CTA pair may signal the barrier of either CTA (bar: a shared::cluster address).
-template <bool kPair>
+template <bool kTwo>
 __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* tm, int x, int y, int z, uint32_t bar) {
-  if constexpr (kPair)
+  if constexpr (kTwo)
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
@@ -90,9 +107,9 @@ __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* tm, int x,
         "l"(tm), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
-template <bool kPair>
+template <bool kTwo>
 __device__ __forceinline__ void load_4d(void* dst, const CUtensorMap* tm, int x, int y, int z, int w, uint32_t bar) {
-  if constexpr (kPair)
+  if constexpr (kTwo)
     asm volatile(
         "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
@@ -106,9 +123,9 @@ __device__ __forceinline__ void load_4d(void* dst, const CUtensorMap* tm, int x,
         : "memory");
 }
 
-template <bool kPair>
+template <bool kTwo>
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (kPair)
+  if constexpr (kTwo)
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
@@ -122,9 +139,9 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
         : "memory");
 }
 // Arrival, on this barrier of the CTAs in `ctas`, when the MMAs issued so far have completed.
-template <bool kPair>
+template <bool kTwo>
 __device__ __forceinline__ void commit(uint64_t* b, int ctas = 3) {
-  if constexpr (kPair)
+  if constexpr (kTwo)
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(b)),
         "h"(static_cast<uint16_t>(ctas))
@@ -152,20 +169,8 @@ __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
-}
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t s) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf16x2(uint64_t v) {
+__device__ __forceinline__ f32x2 pack2(uint32_t lo, uint32_t hi) { return moe::pack2(__uint_as_float(lo), __uint_as_float(hi)); }
+__device__ __forceinline__ uint32_t bf16x2(f32x2 v) {
   const float2 f = unpack2(v);
   const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -268,20 +273,21 @@ struct Items {
   }
 };
 
-template <int BN, bool kPair>
+template <int BN, Mode kMode>
 __global__ void __launch_bounds__(kThreads, 1)
-    block_fp8_kernel(const __grid_constant__ Maps<Tile<BN, kPair>::kBoxes> maps, BlockFp8Args a, bool vec) {
-  using C = Tile<BN, kPair>;
+    block_fp8_kernel(const __grid_constant__ Maps<Tile<BN, kMode>::kBoxes> maps, BlockFp8Args a, bool vec) {
+  using C = Tile<BN, kMode>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ GroupTiles gt;
   __shared__ Bars sm;
+  __shared__ float s_scale[kMode == kFused ? kScaleRing : 1][32];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sA = base;
+  uint8_t* sA = base;                                  // first: the MMA reads 128 rows, past a tile's last into sB
   uint8_t* sB = base + C::kStages * C::kAStage;
   uint8_t* sOut = sB + C::kStages * C::kBStage;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = kPair ? cluster_rank() : 0;    // rank 0 of a pair issues the MMAs
+  const uint32_t rank = C::kTwo ? cluster_rank() : 0;    // rank 0 of a pair issues the MMAs
   const int NT = (a.N + BN - 1) / BN;
   const int KB = (a.K + kChunk - 1) / kChunk, KF = a.K / kChunk;
 
@@ -292,14 +298,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&sm.acc_full[s], 1);
-      mbar_init(&sm.acc_empty[s], C::kWarps * (kPair ? 2 : 1));
+      mbar_init(&sm.acc_empty[s], C::kWarps * (C::kTwo ? 2 : 1));
     }
+    for (int s = 0; s < kScaleRing; ++s) mbar_init(&sm.scales[s], 1);
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWarpAlloc) {
-    if constexpr (kPair) {
+    if constexpr (C::kTwo) {
       asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem_base)),
                    "r"(C::kTmemCols));
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
@@ -309,16 +316,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
   }
-  // Matrices and offsets are read before the wait for the previous launch, the row quantizer: it
-  // lets this kernel start only after its own wait, that is, after everything before it.  Only the
-  // row codes and scales (the row producer, the promotion) depend on the quantizer itself.
+  // Matrices and offsets are read before the wait for the previous launch where that is the row
+  // quantizer: it lets this kernel start only after its own wait, that is, after everything before
+  // it.  Only the row codes and scales (the row producer, the promotion) depend on the quantizer.
+  if (kMode == kFused) pdl_wait();
   build_group_tiles(gt, a.offsets, a.G, a.M, C::kTileRows, a.status);
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_barrier();              // both CTAs' barriers are initialised
+  if constexpr (C::kTwo) cluster_barrier();              // both CTAs' barriers are initialised
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  Items it(kPair ? blockIdx.x / 2 : blockIdx.x, kPair ? gridDim.x / 2 : gridDim.x, NT, gt.first[a.G + 1]);
+  Items it(C::kTwo ? blockIdx.x / 2 : blockIdx.x, C::kTwo ? gridDim.x / 2 : gridDim.x, NT, gt.first[a.G + 1]);
   auto wait = [&](uint64_t* b, uint32_t parity) {
     return mbar_wait_flag(b, parity, &sm.abort_flag, a.status, kWaitTimeoutNs);
   };
@@ -332,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 256 x 208 where a thread promotes 64 columns) fit and compile without spills.  With 36 bytes
     // spilled the dense product took 139 instead of 125 us.
     if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == kWarpTmaB || warp == kWarpTmaA) {
+    else if constexpr (kMode != kFused) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kWarpTmaB || (warp == kWarpTmaA && kMode != kFused)) {
       if (lane == 0) {
         uint32_t is = 0;
         bool ok = true;
@@ -350,18 +358,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < KB; ++kb, ++is) {
             const int st = is % C::kStages;
             if (!(ok = wait(&sm.empty[st], ((is / C::kStages) & 1) ^ 1))) break;
-            const uint32_t bar = kPair ? cluster_addr(&sm.full[st], 0) : smem_u32(&sm.full[st]);
+            const uint32_t bar = C::kTwo ? cluster_addr(&sm.full[st], 0) : smem_u32(&sm.full[st]);
             if (warp == kWarpTmaA) {
-              if (rank == 0) mbar_expect_tx(&sm.full[st], (box0 + (kPair ? box1 : 0)) * 16 * kChunk);
-              load_3d<kPair>(sA + st * C::kAStage, &maps.a[box - 1], 0, rt.row + static_cast<int>(rank) * kRows, kb, bar);
+              if (rank == 0) mbar_expect_tx(&sm.full[st], (box0 + (C::kTwo ? box1 : 0)) * 16 * kChunk);
+              load_3d<C::kTwo>(sA + st * C::kAStage, &maps.a[box - 1], 0, rt.row + static_cast<int>(rank) * kRows, kb, bar);
             } else {
-              if (rank == 0) mbar_expect_tx(&sm.full[st], C::kBStage * (kPair ? 2 : 1));
-              if (kb < KF) load_4d<kPair>(sB + st * C::kBStage, &maps.b, 0, n0, kb, rt.group, bar);
-              else load_3d<kPair>(sB + st * C::kBStage, &maps.b_tail, kb * kChunk, n0, rt.group, bar);
+              if (rank == 0) mbar_expect_tx(&sm.full[st], C::kBStage * (C::kTwo ? 2 : 1));
+              if (kb < KF) load_4d<C::kTwo>(sB + st * C::kBStage, &maps.b, 0, n0, kb, rt.group, bar);
+              else load_3d<C::kTwo>(sB + st * C::kBStage, &maps.b_tail, kb * kChunk, n0, rt.group, bar);
             }
           }
         }
-        if (kPair && ok) {   // the MMAs' last arrivals reach this CTA before it ends
+        if (C::kTwo && ok) {   // the MMAs' last arrivals reach this CTA before it ends
           const uint32_t last = is;
           for (uint32_t j = last > C::kStages ? last - C::kStages : 0; ok && j < last; ++j)
             ok = wait(&sm.empty[j % C::kStages], (j / C::kStages) & 1);
@@ -376,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == kWarpMma && rank == 0) {
-      const uint32_t idesc = idesc_f32acc(kPair ? 256 : 128, BN);
+      const uint32_t idesc = idesc_f32acc(C::kTwo ? 256 : 128, BN);
       uint32_t is = 0, ib = 0;
       bool ok = true;
       for (; ok && it.more(); it.next()) {
@@ -390,15 +398,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t aa = smem_u32(sA + st * C::kAStage), ba = smem_u32(sB + st * C::kBStage);
 #pragma unroll
             for (int kk = 0; kk < kChunk / 32; ++kk)
-              mma_e4m3<kPair>(tmem + buf * BN, smem_desc_sw128(aa + kk * 32), smem_desc_sw128(ba + kk * 32), idesc, kk != 0);
-            commit<kPair>(&sm.acc_full[buf]);
-            commit<kPair>(&sm.empty[st]);
+              mma_e4m3<C::kTwo>(tmem + buf * BN, smem_desc_sw128(aa + kk * 32), smem_desc_sw128(ba + kk * 32), idesc, kk != 0);
+            commit<C::kTwo>(&sm.acc_full[buf]);
+            commit<C::kTwo>(&sm.empty[st]);
           }
           __syncwarp();
         }
       }
       if (elect_one()) {   // every MMA issued completes before TMEM is released (bounded)
-        commit<kPair>(&sm.drain, 1);
+        commit<C::kTwo>(&sm.drain, 1);
         for (uint32_t i = 0; i < kSpinLimit && !mbar_try(&sm.drain, 0); ++i) {
         }
       }
@@ -406,15 +414,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    else if constexpr (kMode != kFused) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int q = warp & 3, wg = (warp - kWarpPromote) >> 2;
-    {
+    if (kMode != kFused || (q == 0 && wg < BN / C::kCols)) {
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + wg * C::kCols;
       const int NB = (a.N + 127) / 128, pitch = (KB + 3) & ~3;
       uint32_t ib = 0;
       bool ok = true;
       const int r0 = static_cast<int>(rank) * kRows + q * 32;   // this warp's first row of the tile
-      uint8_t* stage = sOut + (wg * 4 + q) * C::kBoxesOut * 4096;
+      uint8_t* stage = sOut + (kMode == kFused ? wg : wg * 4 + q) * C::kBoxesOut * 4096;
       // an item and its first scales, read before the previous item is stored
       struct Job {
         int group, row0, rows, n0;             // this warp's rows (none or fewer than 32 at a group's end)
@@ -431,12 +439,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rt.group < a.G) {
           j.sx = a.x_scales + static_cast<int64_t>(lane < j.rows ? j.row0 + lane : rt.row) * pitch;
           j.sw = a.w_scales + (static_cast<int64_t>(rt.group) * NB + min(j.n0 / 128, NB - 1)) * KB;
-          j.x = __ldg(j.sx);
+          if (kMode != kFused) j.x = __ldg(j.sx);
           j.w = __ldg(j.sw);
         }
         return j;
       };
-      pdl_wait();
+      if (kMode != kFused) pdl_wait();
       Job job;
       if (it.more()) job = job_of(it);
       while (ok && it.more()) {
@@ -445,10 +453,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
         if (job.group < a.G) {
           for (int kb = 0; kb < KB; ++kb, ++ib) {
+            if constexpr (kMode == kFused) {
+              const int ring = ib % kScaleRing;
+              if (!(ok = warp_wait(&sm.scales[ring], (ib / kScaleRing) & 1))) break;
+              job.x = s_scale[ring][lane];
+            }
             const uint32_t sc = __float_as_uint(job.x * job.w);
             const uint64_t s2 = pack2(sc, sc);
             if (kb + 1 < KB) {               // the next block's, in flight during this block
-              job.x = __ldg(job.sx + kb + 1);
+              if (kMode != kFused) job.x = __ldg(job.sx + kb + 1);
               job.w = __ldg(job.sw + kb + 1);
             }
             const int buf = ib % C::kBufs;
@@ -458,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_before();
               __syncwarp();
               if (lane == 0) {
-                if constexpr (kPair) arrive_at(cluster_addr(&sm.acc_empty[buf], 0));
+                if constexpr (C::kTwo) arrive_at(cluster_addr(&sm.acc_empty[buf], 0));
                 else mbar_arrive(&sm.acc_empty[buf]);
               }
             };
@@ -472,7 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                 if (c + 32 >= C::kCols) release();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) fma2(acc[c / 2 + j], pack2(v[j / 8][2 * (j % 8)], v[j / 8][2 * (j % 8) + 1]), s2);
+                for (int j = 0; j < 16; ++j)
+                  acc[c / 2 + j] = fma2(pack2(v[j / 8][2 * (j % 8)], v[j / 8][2 * (j % 8) + 1]), s2, acc[c / 2 + j]);
               }
             } else {
               release();
@@ -492,29 +506,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  if constexpr (kMode == kFused) {
+    // Warps 5, 6, 7, 9, 10 and 11 take a block of K each in turn, all rows of the tile, four rows at a
+    // time and eight lanes per row: a block passes from memory to the MMA in about 1000 cycles, so a
+    // warp that took part in every block would hold the stream of the matrices back.
+    const int quantizer = warp < kWarpPromote || (warp & 3) == 0 ? -1 : warp < 8 ? warp - 5 : warp - 6;
+    if (quantizer >= 0 && quantizer < C::kQuantizers) {
+      const int r0 = lane >> 3, col = (lane & 7) * 16;
+      uint32_t is = quantizer;                    // block of the CTA, and its place in the item
+      int kb = quantizer;
+      bool ok = true;
+      for (; ok && it.more(); it.next()) {
+        const RowTile rt = group_tile_warp(gt, a.G, it.tile, C::kTileRows, lane);
+        if (rt.group == a.G) continue;
+        for (; ok && kb < KB; kb += C::kQuantizers, is += C::kQuantizers) {
+          const uint16_t* src = a.x + static_cast<int64_t>(rt.row) * a.K + kb * kChunk + col;
+          auto load = [&](int r, uint4 (&v)[2]) {
+            v[0] = v[1] = make_uint4(0, 0, 0, 0);
+            if (r < rt.rows && kb * kChunk + col < a.K) {
+              const uint4* p = reinterpret_cast<const uint4*>(src + static_cast<int64_t>(r) * a.K);
+              v[0] = __ldg(p);
+              v[1] = __ldg(p + 1);
+            }
+          };
+          const int st = is % C::kStages, ring = is % kScaleRing;
+          uint4 v[2], next[2];
+          load(r0, v);
+          if (!(ok = warp_wait(&sm.empty[st], ((is / C::kStages) & 1) ^ 1))) break;
+          for (int r = r0; r - r0 < rt.rows; r += 4) {
+            load(r + 4, next);
+            float scale;
+            const uint4 codes = quantize_block16(v, lane, scale);
+            *reinterpret_cast<uint4*>(sA + st * C::kAStage + r * kChunk + (((lane & 7) ^ (r & 7)) << 4)) = codes;
+            if ((lane & 7) == 0) s_scale[ring][r] = scale;
+            v[0] = next[0];
+            v[1] = next[1];
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm.scales[ring]);
+            mbar_arrive(&sm.full[st]);
+          }
+        }
+        kb -= KB;
+      }
+    }
+  }
+
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_barrier();   // neither CTA's shared memory or TMEM is used any more
+  if constexpr (C::kTwo) cluster_barrier();   // neither CTA's shared memory or TMEM is used any more
   if (warp == kWarpAlloc) {
     __syncwarp();
     tc_fence_after();
-    if constexpr (kPair)
+    if constexpr (C::kTwo)
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
     else
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols));
   }
 }
 
-template <int BN, bool kPair>
+template <int BN, Mode kMode>
 cudaError_t launch_tile(const BlockFp8Args& a, int n_sm, cudaStream_t st) {
-  using C = Tile<BN, kPair>;
-  auto kern = block_fp8_kernel<BN, kPair>;
+  using C = Tile<BN, kMode>;
+  auto kern = block_fp8_kernel<BN, kMode>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), C::kSmem);
   if (e != cudaSuccess) return e;
   const uint64_t M = a.M, N = a.N, K = a.K, G = a.G, KB = (K + kChunk - 1) / kChunk, KF = K / kChunk;
   Maps<C::kBoxes> maps;
   bool ok = true;
-  for (int i = 0; ok && i < C::kBoxes; ++i) {
+  for (int i = 0; kMode != kFused && ok && i < C::kBoxes; ++i) {
     const uint64_t dims[3] = {kChunk, M, KB}, strides[2] = {KB * kChunk, kChunk};
     const uint32_t box[3] = {kChunk, static_cast<uint32_t>(16 * (i + 1)), 1};
     ok = make_tensor_map(&maps.a[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, a.x_codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
@@ -539,9 +601,9 @@ cudaError_t launch_tile(const BlockFp8Args& a, int n_sm, cudaStream_t st) {
   }
   // tiles at most: one per full tile of rows and one more per group that has rows
   const int64_t most = (M / C::kTileRows + std::min(M, G + 1)) * ((N + BN - 1) / BN);
-  const int64_t ctas = kPair ? std::min<int64_t>(2 * most, n_sm / 2 * 2) : std::min<int64_t>(most, n_sm);
+  const int64_t ctas = C::kTwo ? std::min<int64_t>(2 * most, n_sm / 2 * 2) : std::min<int64_t>(most, n_sm);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(kPair ? 2 : 1, ctas)));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max<int64_t>(C::kTwo ? 2 : 1, ctas)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
@@ -553,7 +615,7 @@ cudaError_t launch_tile(const BlockFp8Args& a, int n_sm, cudaStream_t st) {
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kPair ? 2 : 1;
+  cfg.numAttrs = C::kTwo ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, maps, a, vec);
 }
 
@@ -563,15 +625,23 @@ cudaError_t launch_block_fp8_matmul(const BlockFp8Args& a, cudaStream_t st) {
   int n_sm = 0;
   cudaError_t e = current_sm_count(&n_sm);
   if (e != cudaSuccess) return e;
+  // Up to 16 rows on at most one tile per SM quantize themselves: one launch instead of two (a call
+  // of M = 1, N = K = 256 takes 7.3 instead of 10.7 us, M = 8, N = K = 4096 15 instead of 16 us; 32
+  // such rows 17 instead of 16 us, and where the matrices stream through every SM, 80 rows over 512
+  // of them, 36 instead of 34 us).
+  const int64_t few = std::min<int64_t>(a.M, a.G);   // tiles of rows, at most
+  if (a.M <= 16 && few * ((a.N + 127) / 128) <= n_sm)
+    return few * ((a.N + 63) / 64) <= n_sm ? launch_tile<64, kFused>(a, n_sm, st) : launch_tile<128, kFused>(a, n_sm, st);
+  if ((e = launch_quantize_rows_block(a.x, a.M, a.K, a.x_codes, a.x_scales, st)) != cudaSuccess) return e;
   // Tiles of 128 x 256, at most one partial one per group.  Half as wide while half of the SMs would
   // have none (M = 512, N = K = 4096: 24 against 28 us; M = 1024: 37 against 30 us); pairs of CTAs,
   // which read a third less from L2, where groups fill their 256 rows and K is long enough for the
   // pair's start (N = K = 4096: 75 against 80 us at M = 4096; 640 rows per group, N = 2048: 624
   // against 608 us at K = 512).
   const int64_t row_tiles = a.G == 1 ? (a.M + kRows - 1) / kRows : a.M / kRows + std::min(a.M, a.G);
-  if (2 * row_tiles * ((a.N + 255) / 256) <= n_sm) return launch_tile<128, false>(a, n_sm, st);
-  if (a.M >= 256 * static_cast<int64_t>(a.G) && a.K >= 1024) return launch_tile<256, true>(a, n_sm, st);
-  return launch_tile<256, false>(a, n_sm, st);
+  if (2 * row_tiles * ((a.N + 255) / 256) <= n_sm) return launch_tile<128, kSingle>(a, n_sm, st);
+  if (a.M >= 256 * static_cast<int64_t>(a.G) && a.K >= 1024) return launch_tile<256, kPair>(a, n_sm, st);
+  return launch_tile<256, kSingle>(a, n_sm, st);
 }
 
 }  // namespace moe

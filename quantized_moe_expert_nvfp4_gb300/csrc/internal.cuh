@@ -351,8 +351,9 @@ cudaError_t launch_quantize_blocks(const void* w, bool fp32, int G, int N, int K
 cudaError_t launch_transpose_blocks(const uint8_t* codes, const float* scales, int G, int N, int K, uint8_t* t_codes,
                                     float* t_scales, cudaStream_t st);
 struct BlockFp8Args {
-  const uint8_t* x_codes;       // [M, 128 KB], KB = ceil(K / 128)
-  const float* x_scales;        // [M, KB rounded up to 4]
+  const uint16_t* x;            // [M, K] bf16
+  uint8_t* x_codes;             // [M, 128 KB], KB = ceil(K / 128)
+  float* x_scales;              // [M, KB rounded up to 4]
   const uint8_t* w_codes;       // [G, N, K]
   const float* w_scales;        // [G, ceil(N / 128), KB]
   const int32_t* offsets;       // [G + 1], or NULL: one group of all rows
@@ -361,6 +362,7 @@ struct BlockFp8Args {
   bool out_fp32;
   int32_t* status;
 };
+// The rows' quantization and the product (one launch for few rows, else two).
 cudaError_t launch_block_fp8_matmul(const BlockFp8Args& a, cudaStream_t st);
 
 // Norms before and after a block (block_norm.cu); part: [2][norm_max_parts][H] fp32.

@@ -1,0 +1,51 @@
+// The rule of e4m3 blocks of 128 on bf16 rows whose blocks are held by eight lanes, 16 columns each.
+#pragma once
+
+#include "row_units.cuh"
+
+namespace moe {
+
+// A bf16 pair times inv -> two e4m3 codes (nearest even, saturating), the first in the low byte.
+__device__ __forceinline__ uint16_t codes2(uint32_t pair, f32x2 inv) {
+  const float2 q = unpack2(mul2(pack2(__uint_as_float(pair << 16), __uint_as_float(pair & 0xffff0000u)), inv));
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(q.y), "f"(q.x));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, f32x2 inv) {
+  uint32_t r;
+  asm("mov.b32 %0, {%1, %2};" : "=r"(r) : "h"(codes2(a, inv)), "h"(codes2(b, inv)));
+  return r;
+}
+__device__ __forceinline__ uint4 codes16(const uint4 (&q)[2], f32x2 inv) {
+  return make_uint4(codes4(q[0].x, q[0].y, inv), codes4(q[0].z, q[0].w, inv), codes4(q[1].x, q[1].y, inv),
+                    codes4(q[1].z, q[1].w, inv));
+}
+
+// Largest magnitudes of this lane's 16 values, at even and at odd places (a NaN stays one).
+__device__ __forceinline__ __nv_bfloat162 max16(const uint4 (&q)[2]) {
+  const uint32_t w[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+  __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+  for (int c = 1; c < 8; ++c) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[c])));
+  return m;
+}
+
+// 448 / amax, or (second) amax / 448: one rounded division; 1 for an amax of zero or not finite.
+__device__ __forceinline__ float block_ratio(float amax, bool second) {
+  const bool usable = amax > 0.0f && amax <= 3.402823466e38f;
+  return __fdiv_rn(usable ? (second ? amax : 448.0f) : 1.0f, usable ? (second ? 448.0f : amax) : 1.0f);
+}
+
+// One block per eight lanes: this lane's 16 codes and, in every lane, the block's scale.
+__device__ __forceinline__ uint4 quantize_block16(const uint4 (&q)[2], int lane, float& scale) {
+  const __nv_bfloat162 m = max16(q);
+  __nv_bfloat162 top = __hmax2_nan(m, __lowhigh2highlow(m));
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1) top = __hmax2_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float ratio = block_ratio(__low2float(top), lane & 1);   // inverse in even lanes, scale in odd ones
+  scale = __shfl_sync(0xffffffffu, ratio, lane | 1);
+  return codes16(q, both(__shfl_sync(0xffffffffu, ratio, lane & ~1)));
+}
+
+}  // namespace moe

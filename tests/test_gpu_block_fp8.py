@@ -88,6 +88,9 @@ PRODUCTS = [
     (64, 130, 160, [64, 0, 0], FP), (40, 264, 528, [0, 0, 40], BF), (50, 96, 2064, [17, 0, 20], BF),
     (600, 520, 400, [5, 300, 0, 250, 40], FP), (90, 64, 128, [1] * 90, BF), (33, 72, 112, [0] * 5, FP),
     (1500, 2048, 512, [700, 3, 400, 0, 390], BF), (257, 4096, 256, None, BF), (2050, 320, 1408, [2000, 1, 49], FP),
+    # up to 16 rows, which the product quantizes itself: several blocks per warp, both tile widths
+    (16, 300, 2064, [0, 5, 0, 1, 7, 0], FP), (13, 4096, 400, None, BF), (9, 264, 4112, [2, 0, 3], FP),
+    (16, 9800, 272, None, FP), (11, 1000, 1152, [1] * 9, BF), (1, 72, 4096, None, FP),
     # enough tiles for the large ones: one CTA per tile (many matrices), and pairs of CTAs
     (2500, 1300, 400, [0, 128, 129, 127, 1, 0, 0, 255, 256, 257, 16, 17, 300, 64, 33, 500, 32, 31, 0, 200], FP),
     (5000, 1536, 256, [100] * 45 + [480], BF), (4100, 1300, 272, None, FP), (4224, 2048, 1040, None, BF),
