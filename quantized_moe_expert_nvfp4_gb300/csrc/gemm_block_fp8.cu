@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else if (warp == kWarpMma && rank == 0) {
+      const bool leader = elect_one();
       const uint32_t idesc = idesc_f32acc(C::kTwo ? 256 : 128, BN);
       uint32_t is = 0, ib = 0;
       bool ok = true;
@@ -391,10 +392,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (group_tile_warp(gt, a.G, it.tile, C::kTileRows, lane).group == a.G) continue;
         for (int kb = 0; kb < KB; ++kb, ++is, ++ib) {
           const int st = is % C::kStages, buf = ib % C::kBufs;
-          if (!(ok = warp_wait(&sm.full[st], (is / C::kStages) & 1))) break;
-          if (!(ok = warp_wait(&sm.acc_empty[buf], ((ib / C::kBufs) & 1) ^ 1))) break;
+          // one vote for both waits: this warp's instructions bound the small tiles (M = 64, N = K = 4096:
+          // 15.1 us, with a vote for each wait 16.6)
+          ok = wait(&sm.acc_empty[buf], ((ib / C::kBufs) & 1) ^ 1) && wait(&sm.full[st], (is / C::kStages) & 1);
+          if (!(ok = __all_sync(0xffffffffu, ok) != 0)) break;
           tc_fence_after();
-          if (elect_one()) {
+          if (leader) {
             const uint32_t aa = smem_u32(sA + st * C::kAStage), ba = smem_u32(sB + st * C::kBStage);
 #pragma unroll
             for (int kk = 0; kk < kChunk / 32; ++kk)
