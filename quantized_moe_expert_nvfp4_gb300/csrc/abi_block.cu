@@ -66,7 +66,7 @@ moe_status_t check_norm(const moe_norm_t* s) {
   return MOE_OK;
 }
 
-size_t norm_ws_bytes(int64_t T, int H) { return align256(sizeof(float) * 2 * static_cast<size_t>(norm_max_parts(T, H)) * H); }
+size_t norm_ws_bytes(int64_t T, int H) { return align256(sizeof(float) * 2 * static_cast<size_t>(norm_max_parts(T)) * H); }
 
 }  // namespace
 }  // namespace moe

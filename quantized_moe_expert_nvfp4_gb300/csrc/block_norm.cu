@@ -11,9 +11,9 @@
 // b w' at the end.
 // Rows are read once and stay in registers between the row sums and their use, so every call moves
 // the bytes of its inputs and outputs once and is bound by HBM; weights and gates of a channel stay
-// in registers over the rows that a thread takes.  A group of threads takes a row (one or two units
-// of eight elements per thread), a CTA several groups, and a group's next row is loaded before the
-// current one's sums, whose barriers it would otherwise wait behind.  Sums are fp32 in a fixed
+// in registers or shared memory over the rows that a thread takes.  A group of threads takes a row (one
+// to three units of eight elements per thread), a CTA several groups, and a group's next row is loaded
+// before the current one's sums, whose barriers it would otherwise wait behind.  Sums are fp32 in a fixed
 // order: a row's by shuffles and one array per group, a column's in registers over the group's
 // rows, then over the CTA's groups, written per CTA and summed by a second kernel (no atomics).
 #include <algorithm>
@@ -46,38 +46,50 @@ struct Place {
 };
 
 // Sums of N values over the group, the same bits in every thread of it.  `slot` alternates between
-// calls, so one barrier per call is enough.
+// calls, so one barrier per call is enough.  A group's warps are padded with zeros to a multiple of
+// four, which are written once.
 constexpr int kMaxWarps = 32;
 template <int N>
-__device__ __forceinline__ void group_sum(float (&v)[N], int& slot) {
-  __shared__ __align__(16) float s_sum[2][N][kMaxWarps];
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return;
-  const int first = threadIdx.y * warps, warp = first + (threadIdx.x >> 5);   // groups of more than one warp have 2 or a multiple of 4
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s_sum[slot][i][warp] = v[i];
-  asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float* p = &s_sum[slot][i][first];
-    float t = 0.0f;
-    if (warps == 2) {
-      t = p[0] + p[1];
-    } else {
-      for (int w = 0; w < warps; w += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(p + w);
-        t += (q.x + q.y) + (q.z + q.w);
-      }
-    }
-    v[i] = t;
+struct GroupSum {
+  float (*at)[N][kMaxWarps];
+  int slot = 0;
+  __device__ __forceinline__ GroupSum() {
+    __shared__ __align__(16) float s_sum[2][N][kMaxWarps];
+    at = s_sum;
+    if (blockDim.x % 128 == 0 || blockDim.x <= 64) return;
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 2 * N * kMaxWarps; i += blockDim.x * blockDim.y)
+      (&s_sum[0][0][0])[i] = 0.0f;
+    __syncthreads();
   }
-  slot ^= 1;
-}
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return;
+    const int first = threadIdx.y * (warps == 2 ? 2 : (warps + 3) & ~3);
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) at[slot][i][first + (threadIdx.x >> 5)] = v[i];
+    asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(blockDim.x) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float* p = &at[slot][i][first];
+      float t = 0.0f;
+      if (warps == 2) {
+        t = p[0] + p[1];
+      } else {
+        for (int w = 0; w < warps; w += 4) {
+          const float4 q = *reinterpret_cast<const float4*>(p + w);
+          t += (q.x + q.y) + (q.z + q.w);
+        }
+      }
+      v[i] = t;
+    }
+    slot ^= 1;
+  }
+};
 
 __device__ __forceinline__ Vec8 load_vec(const float* p, int u, float add) {
   Unit8<float> q;
@@ -96,7 +108,7 @@ template <typename R, int U, int kMaxThreads, int kPerSm>
 __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_before_kernel(NormArgs a) {
   Vec8 w[U];
   Unit8<R> qx[U];
-  int slot = 0;
+  GroupSum<1> group_sum;
   const Place at;
   pdl_wait();
   if (at.row < a.T) EACH_UNIT(i) qx[i].load(a.x, at.row * a.units + UNIT(i));
@@ -110,7 +122,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_before_kernel(NormAr
       EACH(c) s = fma2(x[i].p[c], x[i].p[c], s);
     }
     float sum[1] = {sum2(s)};
-    group_sum(sum, slot);
+    group_sum(sum);
     const float rstd = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rstd;
     EACH_UNIT(i) {
@@ -145,7 +157,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_after_kernel(NormArg
   Vec8 w[U], wn[U];                       // w' times a channel's gate
   Unit8<Y> qy[U];
   Unit8<R> qx[U];
-  int slot = 0;
+  GroupSum<1> group_sum;
   const Place at;
   auto load_row = [&](int64_t t) {
     EACH_UNIT(i) {
@@ -170,7 +182,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_after_kernel(NormArg
     }
     if (t + at.stride < a.T) load_row(t + at.stride);
     float sum[1] = {sum2(s)};
-    group_sum(sum, slot);
+    group_sum(sum);
     const float rstd = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[t] = rstd;
     const f32x2 scale = both(a.b * token_gate(a, t) * rstd), ra = both(a.a);
@@ -193,7 +205,7 @@ __global__ void __launch_bounds__(kMaxThreads, kPerSm) norm_after_kernel(NormArg
     }
     if (kNext) {
       sum[0] = sum2(s);
-      group_sum(sum, slot);
+      group_sum(sum);
       const float rn = 1.0f / sqrtf(sum[0] * a.inv_h + a.eps);
       if (threadIdx.x == 0 && a.rstd_next) a.rstd_next[t] = rn;
       EACH_UNIT(i) {
@@ -237,7 +249,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_before_grad_kernel(NormAr
   Unit8<R> qx[U], qr[U];
   Unit8<uint16_t> qd[U];
   float q_rstd = 0.0f;
-  int slot = 0;
+  GroupSum<1> group_sum;
   const Place at;
   auto load_row = [&](int64_t t) {
     EACH_UNIT(i) {
@@ -271,7 +283,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_before_grad_kernel(NormAr
     }
     if (t + at.stride < a.T) load_row(t + at.stride);
     float dot[1] = {sum2(s)};
-    group_sum(dot, slot);
+    group_sum(dot);
     const f32x2 m = both(-dot[0] * a.inv_h);
     EACH_UNIT(i) {
       Vec8 r;
@@ -293,23 +305,29 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_before_grad_kernel(NormAr
 // so the three row sums e oh, u v and oh v are taken together.  A token's gate has the gradient
 // sum(d v); an element's b w' d yh.  The column sum q = sum_t d yh (times a token's or an
 // element's gate) is the branch weight's gradient over b g, and a channel gate's over b w'.
-// kKeep: the vectors of the columns stay in registers and rows are loaded ahead; above 4096 columns
-// (two units per thread) there are no registers for either (4096 x 5120: 104 instead of 112 us).
-template <typename R, typename Y, int U, int kMaxThreads, bool kKeep, bool kNext>
+// One unit per thread keeps the vectors of the columns in registers, and of an element's gate (kElement;
+// a kernel of its own, 51 instead of 68 us for 4096 x 4096) loads the row ahead like the others.  With
+// more units the vectors are in shared memory, 384 threads have 168 registers each, and an element's
+// gate is read where it is used (kElement: either kind of gate).
+template <typename R, typename Y, int U, int kMaxThreads, bool kAhead, bool kElement, bool kNext>
 __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArgs a) {
-  __shared__ Vec8 s_cols[kGradThreads];
-  Vec8 q_col[U], dwn[U], bw[U], wn[U];    // bw: b w' times a channel's gate
+  constexpr bool kKeep = U == 1;
+  extern __shared__ __align__(16) float4 s_vec[];   // !kKeep: [4][units], b w' times a channel's gate, w_next'
+  Vec8 q_col[U], dwn[U];
+  Vec8 bw_kept, wn_kept;
   Unit8<R> qd[U], qo[U];
   Unit8<Y> qy[U];
-  Unit8<uint16_t> qn[U];
+  Unit8<uint16_t> qn[U], qg;
   float q_rstd = 0.0f, q_rn = 0.0f;
-  int slot = 0;
+  GroupSum<kNext ? 3 : 1> group_sum;
   const Place at;
+  const bool by_element = kElement && (kKeep || a.gate_kind == MOE_GATE_ELEMENT);
   auto load_row = [&](int64_t t) {
     EACH_UNIT(i) {
       const int64_t u = t * a.units + UNIT(i);
       qd[i].load(a.dout, u);
       qy[i].load(a.y, u);
+      if (kKeep && by_element) qg.load(a.gate, u);
       if (kNext) {
         qo[i].load(a.x, u);
         qn[i].load(a.dn, u);
@@ -319,44 +337,66 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArg
     if (kNext) q_rn = __ldg(a.rstd_next_in + t);
   };
   pdl_wait();
-  if (kKeep && at.row < a.T) load_row(at.row);
-  auto load_bw = [&](int i) {
-    bw[i] = gated_weight(a, UNIT(i));
-    EACH(c) bw[i].p[c] = mul2(bw[i].p[c], both(a.b));
+  if (kAhead && at.row < a.T) load_row(at.row);
+  auto put = [&](int which, int u, const Vec8& v) {
+    Unit8<float> q;
+    q.set(v);
+    s_vec[which * a.units + u] = q.a;
+    s_vec[(which + 1) * a.units + u] = q.b;
   };
-  EACH_UNIT(i) {
-    if (kKeep) load_bw(i);
-    if (kKeep && kNext) wn[i] = load_vec(a.w_next, UNIT(i), a.w_off);
-    EACH(c) {
-      q_col[i].p[c] = 0;
-      dwn[i].p[c] = 0;
+  auto take = [&](int which, int u) {
+    Unit8<float> q;
+    q.a = s_vec[which * a.units + u];
+    q.b = s_vec[(which + 1) * a.units + u];
+    return q.get();
+  };
+  auto branch_vec = [&](int u) {
+    Vec8 v = gated_weight(a, u);
+    EACH(c) v.p[c] = mul2(v.p[c], both(a.b));
+    return v;
+  };
+  if constexpr (kKeep) {
+    if (UNIT(0) < a.units) {
+      bw_kept = branch_vec(UNIT(0));
+      if (kNext) wn_kept = load_vec(a.w_next, UNIT(0), a.w_off);
     }
+  } else {
+    for (int u = threadIdx.y * blockDim.x + threadIdx.x; u < a.units; u += blockDim.x * blockDim.y) {
+      put(0, u, branch_vec(u));
+      if (kNext) put(2, u, load_vec(a.w_next, u, a.w_off));
+    }
+    __syncthreads();
   }
-  const bool by_element = a.gate_kind == MOE_GATE_ELEMENT;
+#pragma unroll
+  for (int i = 0; i < U; ++i) EACH(c) {
+    q_col[i].p[c] = 0;
+    dwn[i].p[c] = 0;
+  }
   for (int64_t t = at.row; t < a.T; t += at.stride) {
-    if (!kKeep) load_row(t);
+    if (!kAhead) load_row(t);
     const float rstd = q_rstd, rn = q_rn;
     Vec8 d[U], yh[U], oh[U];
+    const Unit8<uint16_t> gate = qg;
     f32x2 s_eo = 0, s_uv = 0, s_ov = 0;
     EACH_UNIT(i) {
       d[i] = qd[i].get();
       yh[i] = qy[i].get();
       EACH(c) yh[i].p[c] = mul2(yh[i].p[c], both(rstd));
-      if (!kKeep) load_bw(i);
+      const Vec8 bw = kKeep ? bw_kept : take(0, UNIT(i));
       Vec8 v;
-      EACH(c) v.p[c] = mul2(yh[i].p[c], bw[i].p[c]);
+      EACH(c) v.p[c] = mul2(yh[i].p[c], bw.p[c]);
       if (by_element) {
-        const Vec8 g = element_gate(a, t * a.units + UNIT(i));
+        const Vec8 g = kKeep ? gate.get() : element_gate(a, t * a.units + UNIT(i));
         EACH(c) v.p[c] = mul2(v.p[c], g.p[c]);
       }
       if (kNext) {
         oh[i] = qo[i].get();
-        if (!kKeep) wn[i] = load_vec(a.w_next, UNIT(i), a.w_off);
+        const Vec8 wn = kKeep ? wn_kept : take(2, UNIT(i));
         Vec8 e = qn[i].get();
         EACH(c) {
           oh[i].p[c] = mul2(oh[i].p[c], both(rn));
           dwn[i].p[c] = fma2(e.p[c], oh[i].p[c], dwn[i].p[c]);
-          e.p[c] = mul2(e.p[c], wn[i].p[c]);
+          e.p[c] = mul2(e.p[c], wn.p[c]);
           d[i].p[c] = fma2(e.p[c], both(rn), d[i].p[c]);
           s_eo = fma2(e.p[c], oh[i].p[c], s_eo);
           s_ov = fma2(oh[i].p[c], v.p[c], s_ov);
@@ -364,16 +404,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArg
       }
       EACH(c) s_uv = fma2(d[i].p[c], v.p[c], s_uv);
     }
-    if (kKeep && t + at.stride < a.T) load_row(t + at.stride);
+    if (kAhead && t + at.stride < a.T) load_row(t + at.stride);
     float dv, back = 0.0f;
-    if (kNext) {
+    if constexpr (kNext) {
       float sums[3] = {sum2(s_eo), sum2(s_uv), sum2(s_ov)};
-      group_sum(sums, slot);
+      group_sum(sums);
       back = -rn * (sums[0] * a.inv_h);
       dv = fmaf(back, sums[2], sums[1]);
     } else {
       float sums[1] = {sum2(s_uv)};
-      group_sum(sums, slot);
+      group_sum(sums);
       dv = sums[0];
     }
     const float gt = token_gate(a, t);
@@ -381,7 +421,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArg
     const f32x2 m = both(-rstd * gt * (dv * a.inv_h)), rg = both(rstd * gt);
     EACH_UNIT(i) {
       const int64_t u = t * a.units + UNIT(i);
-      if (!kKeep) load_bw(i);
+      const Vec8 bw = kKeep ? bw_kept : take(0, UNIT(i));
       if (kNext) EACH(c) d[i].p[c] = fma2(oh[i].p[c], both(back), d[i].p[c]);
       Vec8 r;
       EACH(c) r.p[c] = mul2(d[i].p[c], both(a.a));
@@ -389,24 +429,25 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_after_grad_kernel(NormArg
       q.set(r);
       q.store(a.dx, u);
       if (by_element) {
-        const Vec8 g = element_gate(a, u);
+        const Vec8 g = kKeep ? gate.get() : element_gate(a, u);
         EACH(c) {
-          r.p[c] = mul2(d[i].p[c], mul2(yh[i].p[c], bw[i].p[c]));
+          r.p[c] = mul2(d[i].p[c], mul2(yh[i].p[c], bw.p[c]));
           d[i].p[c] = mul2(d[i].p[c], g.p[c]);
         }
-        Unit8<uint16_t> qg;
-        qg.set(r);
-        qg.store(a.dgate, u);
+        Unit8<uint16_t> qd_gate;
+        qd_gate.set(r);
+        qd_gate.store(a.dgate, u);
       }
       EACH(c) {
         q_col[i].p[c] = fma2(mul2(d[i].p[c], both(gt)), yh[i].p[c], q_col[i].p[c]);
-        d[i].p[c] = fma2(yh[i].p[c], m, mul2(mul2(d[i].p[c], bw[i].p[c]), rg));
+        d[i].p[c] = fma2(yh[i].p[c], m, mul2(mul2(d[i].p[c], bw.p[c]), rg));
       }
       Unit8<Y> qq;
       qq.set(d[i]);
       qq.store(a.dy, u);
     }
   }
+  Vec8* s_cols = reinterpret_cast<Vec8*>(s_vec);   // the groups' sums take the vectors' place
   write_part<U>(a, 0, q_col, s_cols);
   if (kNext) write_part<U>(a, 1, dwn, s_cols);
 }
@@ -449,25 +490,26 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const float* __restri
 // about as many instructions as a unit's arithmetic, and the kernels are bound by their instructions
 // and latencies before HBM: `after` with the next norm of 32768 x 2048 takes 115 us with one unit and
 // 87 us with two, the gradient of `before` of 16384 x 2048 56 and 47 us (2999 x 1000: 11 and 15 us).
-// The gradient of `after` has no registers for a second unit below 4096 columns.
-constexpr int kForwardOneUnit = 32, kBeforeGradOneUnit = 128, kOneUnit = 512;
+constexpr int kForwardOneUnit = 32, kBeforeGradOneUnit = 128;
 constexpr int kForwardThreads = 256;
 constexpr int kMaxSms = 160;     // the workspace holds the column sums of this many CTAs
 
-// Threads of a row: 32, 64 or a multiple of 128.
-int row_threads(int units, int one_unit) {
+// Threads of a row: whole warps (8160 x 2056 `after`: 27 us; in multiples of 128 37); forward, where a
+// CTA has several small rows, 32, 64 or 128 up to 128, which load an SM's four schedulers alike
+// (13106 x 1280 `before`: 14 against 18 us).  The same for `before` and `after`, whose fused next norm
+// has the bits of a separate call.
+int row_threads(int units, int one_unit, bool gradient) {
   const int per = units <= one_unit ? units : (units + 1) / 2;
-  return per <= 32 ? 32 : per <= 64 ? 64 : (per + 127) / 128 * 128;
+  return !gradient && per > 64 && per <= 128 ? 128 : (per + 31) / 32 * 32;
 }
 
 // A launch of as many CTAs as are resident (`per_sm`), with a row per group at least.
 struct NormLaunch {
   dim3 grid, block;
 };
-NormLaunch launch_of(int64_t T, int units, int one_unit, int threads, int per_sm, int n_sm) {
-  const int x = row_threads(units, one_unit);
+NormLaunch launch_of(int64_t T, int x, int threads, int per_sm, int n_sm) {
   const int y = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(threads / x, T / n_sm)));   // few rows: on all SMs
-  const int64_t most = static_cast<int64_t>(n_sm) * std::max(1, per_sm * threads / (x * y));
+  const int64_t most = static_cast<int64_t>(n_sm) * std::max(1, std::min(4, per_sm * threads / (x * y)));
   NormLaunch l;
   l.block = dim3(x, y);
   l.grid = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min((T + y - 1) / y, most))));
@@ -476,10 +518,28 @@ NormLaunch launch_of(int64_t T, int units, int one_unit, int threads, int per_sm
 // CTAs of kForwardThreads per SM: registers allow four of `before` (two: 32768 x 2048 in 52 instead
 // of 43 us) and two of `after`.
 NormLaunch forward_launch(int64_t T, int units, int per_sm, int n_sm) {
-  return launch_of(T, units, kForwardOneUnit, kForwardThreads, per_sm, n_sm);
+  return launch_of(T, row_threads(units, kForwardOneUnit, false), kForwardThreads, per_sm, n_sm);
 }
-NormLaunch grad_launch(int64_t T, int units, int one_unit, int n_sm) {
-  return launch_of(T, units, one_unit, kGradThreads, 1, std::min(n_sm, kMaxSms));
+// Gradients: one CTA per SM at most, each writes a row of column sums.
+NormLaunch grad_launch(int64_t T, int x, int threads, int n_sm) {
+  n_sm = std::min(n_sm, kMaxSms);
+  NormLaunch l;
+  l.block = dim3(x, static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(threads / x, (T + n_sm - 1) / n_sm))));
+  l.grid = dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>((T + l.block.y - 1) / l.block.y, n_sm))));
+  return l;
+}
+
+// Units per thread of the gradient of `after` (one: 512 threads, two or three: 384).  Two pay off once the
+// groups, of 1.5 times the rows in flight, have several rows each (16384 x 2048: 73 against 78 us,
+// 608 x 2048 8.2 against 7.2, 608 x 1280 6.5 against 7.0), and where one unit leaves an SM a single
+// group (4080 x 2056: 29 against 37 us) or would need more than 512 threads (1638 x 5120: 28 us; two
+// units at 128 registers, with nothing loaded ahead, 47); not for an element's gate, which one unit
+// loads ahead, nor where two units, too, are one group (2048 x 4096: 30 against 28 us).  Three hold
+// the rows that two do not (910 x 9216: 43 us against 63 with two in 64 registers).
+int after_grad_units(int64_t T, int units, int gate, int n_sm) {
+  if (units <= 128 || (units <= 256 && T < (units <= 192 ? 4 : 20) * n_sm)) return 1;
+  if (units <= 512 && (units > 384 || gate == MOE_GATE_ELEMENT)) return 1;
+  return units > 768 && units <= 1152 ? 3 : 2;
 }
 
 NormArgs args_of(const moe_norm_t& s) {
@@ -498,13 +558,14 @@ NormArgs args_of(const moe_norm_t& s) {
 // Launch bounds of 256 x 2 or 512 threads leave 128 registers, those of 256 x 4 or 1024 (above 8192
 // columns) 64, some of them spilled in the latter.
 #define PICK_FORWARD(one, two, wide, more) (s.H / 8 <= kForwardOneUnit ? one : s.H / 8 <= 512 ? two : s.H / 8 <= 1024 ? wide : more)
-#define PICK_GRADIENT(one, two, more) (s.H / 8 <= kOneUnit ? one : s.H / 8 <= 2 * kOneUnit ? two : more)
 #define PICK_BEFORE(K, R) PICK_FORWARD((K<R, 1, 256, 4>), (K<R, 2, 256, 4>), (K<R, 2, 512, 2>), (K<R, 2, 1024, 1>))
-#define PICK_GRAD(K, R) (s.H / 8 <= kBeforeGradOneUnit ? K<R, 1, 512> : s.H / 8 <= 2 * kOneUnit ? K<R, 2, 512> : K<R, 2, 1024>)
+#define PICK_GRAD(K, R) (s.H / 8 <= kBeforeGradOneUnit ? K<R, 1, 512> : s.H / 8 <= 1024 ? K<R, 2, 512> : K<R, 2, 1024>)
 #define PICK_AFTER(K, R, Y, next) \
   PICK_FORWARD((K<R, Y, 1, 256, 2, next>), (K<R, Y, 2, 256, 2, next>), (K<R, Y, 2, 512, 1, next>), (K<R, Y, 2, 1024, 1, next>))
-#define PICK_AFTER_GRAD(K, R, Y, next) \
-  PICK_GRADIENT((K<R, Y, 1, 512, true, next>), (K<R, Y, 2, 512, false, next>), (K<R, Y, 2, 1024, false, next>))
+#define PICK_AFTER_GRAD(K, R, Y, next)                                                          \
+  (per == 1 ? (s.gate == MOE_GATE_ELEMENT ? K<R, Y, 1, 512, true, true, next> : K<R, Y, 1, 512, true, false, next>) \
+   : per == 3 ? K<R, Y, 3, 384, false, true, next>                                              \
+   : s.H / 8 <= 768 ? K<R, Y, 2, 384, true, true, next> : K<R, Y, 2, 1024, false, true, next>)
 #define PICK_NEXT(PICK, K, R, Y) (next ? PICK(K, R, Y, true) : PICK(K, R, Y, false))
 #define PICK_TYPES(PICK, K)                                                                                          \
   (s.residual_fp32 ? (s.branch_fp32 ? PICK_NEXT(PICK, K, float, float) : PICK_NEXT(PICK, K, float, uint16_t))        \
@@ -513,9 +574,7 @@ NormArgs args_of(const moe_norm_t& s) {
 }  // namespace
 
 // CTAs that write column sums, at most (the size of the workspace).
-int64_t norm_max_parts(int64_t T, int H) {
-  return std::max(grad_launch(T, H / 8, kBeforeGradOneUnit, kMaxSms).grid.x, grad_launch(T, H / 8, kOneUnit, kMaxSms).grid.x);
-}
+int64_t norm_max_parts(int64_t T) { return std::max<int64_t>(1, std::min<int64_t>(T, kMaxSms)); }
 
 cudaError_t launch_norm_before(const moe_norm_t& s, const void* x, const float* w, void* n, float* rstd, cudaStream_t st) {
   int n_sm = 0;
@@ -565,7 +624,7 @@ cudaError_t launch_norm_before_grad(const moe_norm_t& s, const void* dn, const v
   a.dres = dres;
   a.dx = dx;
   a.part = part;
-  const NormLaunch l = grad_launch(s.T, a.units, kBeforeGradOneUnit, n_sm);
+  const NormLaunch l = grad_launch(s.T, row_threads(a.units, kBeforeGradOneUnit, true), kGradThreads, n_sm);
   const int grid = static_cast<int>(l.grid.x);
   auto kern = s.residual_fp32 ? PICK_GRAD(norm_before_grad_kernel, float) : PICK_GRAD(norm_before_grad_kernel, uint16_t);
   e = launch_pdl(true, kern, l.grid, l.block, 0, st, a);
@@ -596,11 +655,15 @@ cudaError_t launch_norm_after_grad(const moe_norm_t& s, const void* dout, const 
   a.dx = dx;
   a.dgate = dgate;
   a.part = part;
-  const NormLaunch l = grad_launch(s.T, a.units, kOneUnit, n_sm);
+  const int per = after_grad_units(s.T, a.units, s.gate, n_sm);
+  const NormLaunch l = grad_launch(s.T, (a.units + 32 * per - 1) / (32 * per) * 32, per == 1 ? kGradThreads : 384, n_sm);
   const int grid = static_cast<int>(l.grid.x);
   const bool next = w_next != nullptr;
   auto kern = PICK_TYPES(PICK_AFTER_GRAD, norm_after_grad_kernel);
-  e = launch_pdl(true, kern, l.grid, l.block, 0, st, a);
+  const int vectors = per == 1 ? 0 : a.units * 64, sums = static_cast<int>((l.block.y - 1) * l.block.x * sizeof(Vec8));
+  const int smem = std::max(vectors, sums);
+  if ((e = ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) != cudaSuccess) return e;
+  e = launch_pdl(true, kern, l.grid, l.block, smem, st, a);
   if (e != cudaSuccess) return e;
   const bool channel = s.gate == MOE_GATE_CHANNEL;
   return launch_pdl(true, norm_columns_kernel, dim3((s.H + 31) / 32, next ? 2 : 1), dim3(256), 0, st,

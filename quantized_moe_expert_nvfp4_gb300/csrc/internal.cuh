@@ -366,7 +366,7 @@ struct BlockFp8Args {
 cudaError_t launch_block_fp8_matmul(const BlockFp8Args& a, cudaStream_t st);
 
 // Norms before and after a block (block_norm.cu); part: [2][norm_max_parts][H] fp32.
-int64_t norm_max_parts(int64_t T, int H);
+int64_t norm_max_parts(int64_t T);
 cudaError_t launch_norm_before(const moe_norm_t& s, const void* x, const float* w, void* n, float* rstd, cudaStream_t st);
 cudaError_t launch_norm_before_grad(const moe_norm_t& s, const void* dn, const void* x, const float* w, const float* rstd,
                                     const void* dres, void* dx, float* dw, float* part, cudaStream_t st);

@@ -15,6 +15,9 @@ CASES = [
     (33, 1000, FP, BF, "element", False, 0.0), (700, 264, FP, FP, "channel", True, 1.0), (5, 4096, BF, BF, "element", True, 0.0),
     (64, 4104, FP, BF, "channel", True, 0.0), (19, 16384, BF, FP, "token", True, 0.0), (3, 8200, FP, FP, "none", False, 1.0),
     (2000, 96, BF, BF, "token", False, 0.0), (1301, 520, BF, BF, "channel", False, 0.0),
+    (701, 1288, BF, BF, "channel", True, 0.0), (650, 2080, FP, FP, "token", True, 1.0), (37, 2504, BF, FP, "channel", True, 0.0),
+    (161, 3200, BF, BF, "element", True, 0.0), (21, 4608, FP, FP, "element", True, 0.0), (170, 776, FP, BF, "element", True, 1.0),
+    (9, 6152, BF, BF, "channel", True, 0.0), (6, 9208, FP, FP, "element", True, 0.0), (5, 9224, BF, BF, "element", True, 1.0),
 ]
 IDS = lambda c: f"T{c[0]}_H{c[1]}_{c[4]}{'_next' if c[5] else ''}"  # noqa: E731
 
