@@ -267,10 +267,10 @@ struct Elems<float> {
 __device__ __forceinline__ int routed_row(int p, int64_t S) { return p >= 0 && p < S ? p : -1; }
 
 // out[t] = sum_j w[t, j] rows[p] (+ shared[t]); w == NULL: weights 1 (the gradient of the sort).
-// A group of threads (threadIdx.y) per token, a thread per 16-byte unit; the loads of kTogether ranks
-// are issued together (four: 32768 x 2048, k = 10 takes 234 us, with two 269, with eight 253, which
+// A group of threads (threadIdx.y) per token, kUnits 16-byte units per thread; the loads of kTogether
+// ranks are issued together (four: 32768 x 2048, k = 10 takes 235 us, with two 269, with eight 253, which
 // leave fewer CTAs per SM).
-template <typename V, int kTogether>
+template <typename V, int kTogether, int kUnits>
 __global__ void __launch_bounds__(kThreads) return_kernel(const uint4* __restrict__ rows,
                                                           const int32_t* __restrict__ slot_pos,
                                                           const float* __restrict__ w, const uint4* __restrict__ shared,
@@ -280,12 +280,14 @@ __global__ void __launch_bounds__(kThreads) return_kernel(const uint4* __restric
   pdl_wait();
   if (t >= T) return;
   const int64_t S = T * k;
-  for (int u = threadIdx.x; u < units; u += blockDim.x) {
-    float acc[n];
+  for (int u0 = threadIdx.x; u0 < units; u0 += blockDim.x * kUnits) {
+    float acc[kUnits][n];
 #pragma unroll
-    for (int i = 0; i < n; ++i) acc[i] = 0.0f;
+    for (int v = 0; v < kUnits; ++v)
+#pragma unroll
+      for (int i = 0; i < n; ++i) acc[v][i] = 0.0f;
     for (int j0 = 0; j0 < k; j0 += kTogether) {
-      uint4 q[kTogether];
+      uint4 q[kTogether][kUnits];
       float wj[kTogether];
       bool take[kTogether];
 #pragma unroll
@@ -295,46 +297,62 @@ __global__ void __launch_bounds__(kThreads) return_kernel(const uint4* __restric
           const int p = routed_row(__ldg(slot_pos + t * k + j0 + i), S);
           take[i] = p >= 0;
           wj[i] = w ? __ldg(w + t * k + j0 + i) : 1.0f;
-          if (take[i]) q[i] = __ldg(rows + static_cast<int64_t>(p) * units + u);
+#pragma unroll
+          for (int v = 0; v < kUnits; ++v) {
+            const int u = u0 + v * blockDim.x;
+            if (take[i] && u < units) q[i][v] = __ldg(rows + static_cast<int64_t>(p) * units + u);
+          }
         }
       }
 #pragma unroll
       for (int i = 0; i < kTogether; ++i) {
         if (take[i]) {
-          float f[n];
-          Elems<V>::get(q[i], f);
 #pragma unroll
-          for (int c = 0; c < n; ++c) acc[c] = fmaf(wj[i], f[c], acc[c]);
+          for (int v = 0; v < kUnits; ++v) {
+            float f[n];
+            Elems<V>::get(q[i][v], f);
+#pragma unroll
+            for (int c = 0; c < n; ++c) acc[v][c] = fmaf(wj[i], f[c], acc[v][c]);
+          }
         }
       }
     }
-    if (shared) {
-      float f[n];
-      Elems<V>::get(__ldg(shared + t * units + u), f);
 #pragma unroll
-      for (int c = 0; c < n; ++c) acc[c] += f[c];
+    for (int v = 0; v < kUnits; ++v) {
+      const int u = u0 + v * blockDim.x;
+      if (u >= units) break;
+      if (shared) {
+        float f[n];
+        Elems<V>::get(__ldg(shared + t * units + u), f);
+#pragma unroll
+        for (int c = 0; c < n; ++c) acc[v][c] += f[c];
+      }
+      out[t * units + u] = Elems<V>::put(acc[v]);
     }
-    out[t * units + u] = Elems<V>::put(acc);
   }
 }
 
-// The gradient of the weighted return, TX threads per token: for each rank the row w dout[t] (zeros
-// for a dropped slot) and the dot product of dout[t] with the rank's row.  kTogether ranks have their
-// rows in flight at a time: one where many tokens keep HBM busy (in few registers, eight CTAs per SM;
-// two at a time took 504 instead of 452 us for 32768 x 2048, k = 10), four where a token's own
-// latency counts.
-template <typename V, int TX, int kTogether>
-__global__ void __launch_bounds__(kThreads) return_grad_kernel(const uint4* __restrict__ dout,
+// The gradient of the weighted return, a group of whole warps per token: for each rank the row w dout[t]
+// (zeros for a dropped slot) and the dot product of dout[t] with the rank's row.  kTogether ranks have
+// their rows in flight at a time, at the most CTAs per SM whose registers hold them: 32768 x 2048, k = 10
+// takes 430 us with two (six CTAs; five: 456), 446 with one (eight).  kOnce: a thread has one unit at
+// most, whose dout stays in a register (8192 x 1024, k = 8: 48 instead of 55 us).
+template <typename V, int kTogether, bool kOnce>
+__global__ void __launch_bounds__(kThreads, kTogether == 4 ? 1 : kTogether == 3 ? 5 : 6) return_grad_kernel(const uint4* __restrict__ dout,
                                                                const uint4* __restrict__ ys,
                                                                const int32_t* __restrict__ slot_pos,
                                                                const float* __restrict__ w, int64_t T, int units, int k,
                                                                uint4* __restrict__ dys, float* __restrict__ dw) {
-  constexpr int n = Elems<V>::n, TY = kThreads / TX, kTokenWarps = TX / 32;
-  __shared__ float s_dot[TY][kMaxK][kTokenWarps];
-  const int x = threadIdx.x % TX, y = threadIdx.x / TX, lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * TY + y, S = T * k;
+  constexpr int n = Elems<V>::n;
+  __shared__ float s_dot[kWarps][kMaxK];   // of each warp; a token has whole warps, which leave together
+  const int x = threadIdx.x;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y, S = T * k;
+  const int parts = blockDim.x / 32, part0 = threadIdx.y * parts;
   pdl_wait();
   if (t < T) {
+    uint4 dq = make_uint4(0, 0, 0, 0);
+    if (kOnce && x < units) dq = __ldg(dout + t * units + x);
+#pragma unroll 1
     for (int j0 = 0; j0 < k; j0 += kTogether) {
       int p[kTogether], place[kTogether];
       float wj[kTogether], dot[kTogether];
@@ -348,13 +366,13 @@ __global__ void __launch_bounds__(kThreads) return_grad_kernel(const uint4* __re
         wj[i] = p[i] >= 0 ? __ldg(w + t * k + j0 + i) : 0.0f;
         dot[i] = 0.0f;
       }
-      for (int u = x; u < units; u += TX) {
+      auto unit = [&](int u) {
         uint4 q[kTogether];
 #pragma unroll
         for (int i = 0; i < kTogether; ++i)
           if (p[i] >= 0) q[i] = __ldg(ys + static_cast<int64_t>(p[i]) * units + u);
         float d[n];
-        Elems<V>::get(__ldg(dout + t * units + u), d);
+        Elems<V>::get(kOnce ? dq : __ldg(dout + t * units + u), d);
 #pragma unroll
         for (int i = 0; i < kTogether; ++i) {
           float r[n];
@@ -367,27 +385,36 @@ __global__ void __launch_bounds__(kThreads) return_grad_kernel(const uint4* __re
           for (int c = 0; c < n; ++c) r[c] = p[i] >= 0 ? wj[i] * d[c] : 0.0f;
           if (place[i] >= 0) dys[static_cast<int64_t>(place[i]) * units + u] = Elems<V>::put(r);
         }
+      };
+      if constexpr (kOnce) {
+        if (x < units) unit(x);
+      } else {
+#pragma unroll (kTogether == 1 ? 2 : 1)
+        for (int u = x; u < units; u += blockDim.x) unit(u);
       }
 #pragma unroll
       for (int i = 0; i < kTogether; ++i) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], d);
-        if (lane == 0 && (kTogether == 1 || j0 + i < k)) s_dot[y][j0 + i][x / 32] = dot[i];
+        if (x % 32 == 0 && (kTogether == 1 || j0 + i < k)) s_dot[part0 + x / 32][j0 + i] = dot[i];
       }
     }
   }
   __syncthreads();
-  if (t < T && x < k) {
+  if (t >= T) return;
+  for (int j = x; j < k; j += blockDim.x) {
     float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kTokenWarps; ++i) v += s_dot[y][x][i];
-    dw[t * k + x] = v;
+    for (int i = 0; i < parts; ++i) v += s_dot[part0 + i][j];
+    dw[t * k + j] = v;
   }
 }
 
-// Threads of a token's row (a multiple of 32, one per unit up to kThreads) x tokens of a CTA.
-dim3 token_block(int units) {
-  const int warps = std::min(kWarps, (units + 31) / 32);
+// Threads of a token's row x tokens of a CTA.  Whole warps: as few as hold the row in the fewest rounds of up
+// to kThreads threads (return of 3640 x 2304, k = 8: 25 us; rounds of kThreads 31), or all of the first
+// round's (the sort, whose first round is loaded ahead: 30 against 31 us).
+dim3 token_block(int units, bool even_rounds = true) {
+  const int rounds = even_rounds ? (units + kThreads - 1) / kThreads : 1;
+  const int warps = std::min(kWarps, (units + 32 * rounds - 1) / (32 * rounds));
   return dim3(32 * warps, kWarps / warps);
 }
 
@@ -403,7 +430,7 @@ int chunk_of(int64_t S) {
 int64_t sort_chunks(int64_t S) { return (S + chunk_of(S) - 1) / chunk_of(S); }
 
 // Up to this many slots every CTA counts the ranks itself; above, the counting sort's three launches
-// (T = 204, k = 10: 11.8 us, T = 205: 15.4 us).
+// (T = 204, k = 10: 12.3 us, T = 205: 13.2 us).
 constexpr int kRankMaxSlots = 2048;
 
 cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t* ids, void* xs, int32_t* offsets,
@@ -415,7 +442,7 @@ cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t*
   if (S <= kRankMaxSlots)
     return launch_pdl(true, sort_rank_kernel, dim3(s.T), dim3(kThreads), sizeof(int) * S, st, xv, ids, s.T, units, s.E, s.k,
                       xo, offsets, sorted_slot, slot_pos, status);
-  const dim3 block = token_block(units);
+  const dim3 block = token_block(units, false);
   const int chunk = chunk_of(S), chunks = static_cast<int>(sort_chunks(S));
   const int smem = static_cast<int>(sizeof(int)) * (kPlaceWarps + 2) * (s.E + 1);
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(sort_place_kernel), smem);
@@ -433,9 +460,17 @@ cudaError_t launch_sort_tokens(const SortShape& s, const void* x, const int32_t*
 cudaError_t launch_return_tokens(const SortShape& s, const void* rows, const int32_t* slot_pos, const float* w,
                                  const void* shared, void* out, cudaStream_t st) {
   const int units = units_of(s);
-  const dim3 block = token_block(units);
-  auto kern = s.k <= 2 ? (s.fp32 ? return_kernel<float, 2> : return_kernel<uint16_t, 2>)
-                       : (s.fp32 ? return_kernel<float, 4> : return_kernel<uint16_t, 4>);
+  // loads in flight of a thread: four ranks (three where that makes even rounds), or of one or two ranks
+  // more units (16384 x 2048, k = 1: 25 us with four, 37 with one; 10000 x 2048, k = 2: 22 against 32)
+  const int per = s.k == 1 ? 4 : s.k == 2 ? 2 : 1;
+  const int rounds = (s.k + 3) / 4, together = (s.k + rounds - 1) / rounds;
+  const dim3 block = token_block((units + per - 1) / per);
+  auto pick = [&](auto v) {
+    using V = decltype(v);
+    return s.k == 1 ? return_kernel<V, 1, 4> : s.k == 2 ? return_kernel<V, 2, 2>
+           : together == 3 ? return_kernel<V, 3, 1> : return_kernel<V, 4, 1>;
+  };
+  auto kern = s.fp32 ? pick(float{}) : pick(uint16_t{});
   return launch_pdl(true, kern, dim3((s.T + block.y - 1) / block.y), block, 0, st, static_cast<const uint4*>(rows), slot_pos,
                     w, static_cast<const uint4*>(shared), static_cast<int64_t>(s.T), units, s.k, static_cast<uint4*>(out));
 }
@@ -446,20 +481,24 @@ cudaError_t launch_return_tokens_grad(const SortShape& s, const void* dout, cons
   int n_sm = 0;
   cudaError_t e = current_sm_count(&n_sm);
   if (e != cudaSuccess) return e;
-  auto launch = [&](auto one, auto four, int tokens) {   // tokens of a CTA
-    const int ctas = (s.T + tokens - 1) / tokens;
-    return launch_pdl(true, ctas <= 4 * n_sm ? four : one, dim3(ctas), dim3(kThreads), 0, st,
-                      static_cast<const uint4*>(dout), static_cast<const uint4*>(ys), slot_pos, w,
-                      static_cast<int64_t>(s.T), units, s.k, static_cast<uint4*>(dys), dw);
-  };
+  // Two ranks at a time, three where only that divides them (8000 x 2048, k = 3: 42 against 44 us); four
+  // where the SMs have few CTAs and a token's own latency counts; a single rank by 64 threads, several
+  // units each (16384 x 2048: 34 against 45 us).
+  dim3 block = token_block(units);
+  const bool few = (s.T + block.y - 1) / block.y <= 4 * static_cast<unsigned>(n_sm);
+  if (s.k == 1 && !few) block = token_block(std::min(units, 64));
+  const unsigned ctas = (s.T + block.y - 1) / block.y;
+  const bool once = units <= static_cast<int>(block.x);
   auto pick = [&](auto v) {
     using V = decltype(v);
-    if (units <= 32) return launch(return_grad_kernel<V, 32, 1>, return_grad_kernel<V, 32, 4>, 8);
-    if (units <= 64) return launch(return_grad_kernel<V, 64, 1>, return_grad_kernel<V, 64, 4>, 4);
-    if (units <= 128) return launch(return_grad_kernel<V, 128, 1>, return_grad_kernel<V, 128, 4>, 2);
-    return launch(return_grad_kernel<V, 256, 1>, return_grad_kernel<V, 256, 4>, 1);
+    if (few) return once ? return_grad_kernel<V, 4, true> : return_grad_kernel<V, 4, false>;
+    if (s.k == 1) return return_grad_kernel<V, 1, false>;
+    if (s.k % 2 && s.k % 3 == 0) return once ? return_grad_kernel<V, 3, true> : return_grad_kernel<V, 3, false>;
+    return once ? return_grad_kernel<V, 2, true> : return_grad_kernel<V, 2, false>;
   };
-  return s.fp32 ? pick(float{}) : pick(uint16_t{});
+  auto kern = s.fp32 ? pick(float{}) : pick(uint16_t{});
+  return launch_pdl(true, kern, dim3(ctas), block, 0, st, static_cast<const uint4*>(dout), static_cast<const uint4*>(ys),
+                    slot_pos, w, static_cast<int64_t>(s.T), units, s.k, static_cast<uint4*>(dys), dw);
 }
 
 }  // namespace moe

@@ -15,6 +15,8 @@ CASES = [
     (1, 8, 1, 1, 0.0, BF), (1, 2048, 512, 10, 0.0, BF), (8, 2048, 512, 10, 0.1, BF), (7, 24, 3, 3, 0.3, FP),
     (64, 1000, 40, 6, 0.2, FP), (204, 256, 16, 10, 0.05, BF), (205, 256, 16, 10, 0.05, BF), (300, 136, 1024, 16, 0.02, BF),
     (2500, 264, 33, 4, 0.0, FP), (1024, 64, 1, 1, 0.5, BF), (3000, 4104, 8, 2, 0.01, BF), (37, 16384, 5, 5, 0.1, FP),
+    (3001, 2312, 8, 3, 0.1, BF), (700, 2056, 20, 9, 0.05, BF), (1300, 520, 9, 5, 0.1, FP), (2501, 1040, 7, 1, 0.2, BF),
+    (6, 2600, 4, 1, 0.0, FP), (650, 2304, 11, 6, 0.1, BF),
 ]
 IDS = lambda c: f"T{c[0]}_H{c[1]}_E{c[2]}_k{c[3]}_{'f32' if c[5] == FP else 'bf16'}"  # noqa: E731
 
