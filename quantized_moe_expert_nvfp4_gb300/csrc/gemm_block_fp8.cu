@@ -13,7 +13,11 @@
 //   warp 1      MMA issuer
 //   warp 2      TMA producer of the row tiles (boxes of 16 to 128 rows)
 //   warp 3      TMEM allocation
-//   warps 4-11  promotion and stores: two warpgroups, half of the tile's columns each
+//   warps 4-11  promotion and stores: two warpgroups, half of the tile's columns each (tiles of 64
+//               columns: the first); in kFused the warps of TMEM lanes 0 to 31, and most others
+//               quantize rows
+// Measured: 8192 x 4096 x 4096 with its quantizer 117 us (2.35 PFLOP/s), 40960 rows of 2048 over 512
+// matrices of 1024 rows 225 us, 80 such rows 31 us (148 MB of matrices: 4.8 TB/s with start and tail).
 // An accumulator row that belongs to no row of the tile is fed by whatever shared memory holds and
 // is never read.  Every mbarrier wait is bounded; on timeout the kernel records
 // MOE_ERR_DEVICE_TIMEOUT and winds down.
@@ -60,6 +64,7 @@ struct Tile {
   static constexpr int kBufs = std::min(4, 512 / BN);          // TMEM accumulators
   static constexpr int kTmemCols = kBufs * BN;
   static constexpr int kCols = std::max(64, BN / kPromoteWgs);          // columns per promoting thread
+  static constexpr int kStep = kCols == 64 ? 64 : 32;          // of them read from TMEM at a time
   static constexpr int kBoxes = kMode == kFused ? 1 : kRows / 16;
   static constexpr int kWarps = BN / kCols * (kARows / 32);    // promoting warps
   static constexpr int kBoxesOut = kCols / 64;                 // staged boxes of 32 rows x 128 bytes per warp
@@ -386,22 +391,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kWarpMma && rank == 0) {
       const bool leader = elect_one();
       const uint32_t idesc = idesc_f32acc(C::kTwo ? 256 : 128, BN);
+      // descriptors advance by their address field (16-byte units)
+      const uint64_t a_desc = smem_desc_sw128(smem_u32(sA)), b_desc = smem_desc_sw128(smem_u32(sB));
       uint32_t is = 0, ib = 0;
       bool ok = true;
       for (; ok && it.more(); it.next()) {
         if (group_tile_warp(gt, a.G, it.tile, C::kTileRows, lane).group == a.G) continue;
         for (int kb = 0; kb < KB; ++kb, ++is, ++ib) {
           const int st = is % C::kStages, buf = ib % C::kBufs;
-          // one vote for both waits: this warp's instructions bound the small tiles (M = 64, N = K = 4096:
-          // 15.1 us, with a vote for each wait 16.6)
-          ok = wait(&sm.acc_empty[buf], ((ib / C::kBufs) & 1) ^ 1) && wait(&sm.full[st], (is / C::kStages) & 1);
+          // One vote for both waits, which are tried together: this warp's instructions and the promoting
+          // warps', about 500 cycles a block, bound the small tiles (M = 64, N = K = 4096: with a vote for
+          // each wait 16.6 instead of 15.1 us).
+          const uint32_t pa = ((ib / C::kBufs) & 1) ^ 1, pf = (is / C::kStages) & 1;
+          const bool ra = mbar_try(&sm.acc_empty[buf], pa), rf = mbar_try(&sm.full[st], pf);   // in flight together
+          ok = (ra || wait(&sm.acc_empty[buf], pa)) && (rf || wait(&sm.full[st], pf));
           if (!(ok = __all_sync(0xffffffffu, ok) != 0)) break;
           tc_fence_after();
           if (leader) {
-            const uint32_t aa = smem_u32(sA + st * C::kAStage), ba = smem_u32(sB + st * C::kBStage);
+            const uint64_t ad = a_desc + st * (C::kAStage / 16), bd = b_desc + st * (C::kBStage / 16);
 #pragma unroll
             for (int kk = 0; kk < kChunk / 32; ++kk)
-              mma_e4m3<C::kTwo>(tmem + buf * BN, smem_desc_sw128(aa + kk * 32), smem_desc_sw128(ba + kk * 32), idesc, kk != 0);
+              mma_e4m3<C::kTwo>(tmem + buf * BN, ad + kk * 2, bd + kk * 2, idesc, kk != 0);
             commit<C::kTwo>(&sm.acc_full[buf]);
             commit<C::kTwo>(&sm.empty[st]);
           }
@@ -419,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     else if constexpr (kMode != kFused) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int q = warp & 3, wg = (warp - kWarpPromote) >> 2;
-    if (kMode != kFused || (q == 0 && wg < BN / C::kCols)) {
+    if (wg < BN / C::kCols && (kMode != kFused || q == 0)) {
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(q * 32) << 16) + wg * C::kCols;
       const int NB = (a.N + 127) / 128, pitch = (KB + 3) & ~3;
       uint32_t ib = 0;
@@ -456,20 +466,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < C::kCols / 2; ++i) acc[i] = 0;
         if (job.group < a.G) {
           for (int kb = 0; kb < KB; ++kb, ++ib) {
-            if constexpr (kMode == kFused) {
-              const int ring = ib % kScaleRing;
-              if (!(ok = warp_wait(&sm.scales[ring], (ib / kScaleRing) & 1))) break;
-              job.x = s_scale[ring][lane];
-            }
+            const int buf = ib % C::kBufs, ring = ib % kScaleRing;
+            const uint32_t pb = (ib / C::kBufs) & 1, pr = (ib / kScaleRing) & 1;
+            const bool rb = mbar_try(&sm.acc_full[buf], pb), rr = kMode != kFused || mbar_try(&sm.scales[ring], pr);
+            ok = (rb || wait(&sm.acc_full[buf], pb)) && (rr || wait(&sm.scales[ring], pr));
+            if (!(ok = __all_sync(0xffffffffu, ok) != 0)) break;
+            tc_fence_after();
+            if constexpr (kMode == kFused) job.x = s_scale[ring][lane];
             const uint32_t sc = __float_as_uint(job.x * job.w);
             const uint64_t s2 = pack2(sc, sc);
             if (kb + 1 < KB) {               // the next block's, in flight during this block
               if (kMode != kFused) job.x = __ldg(job.sx + kb + 1);
               job.w = __ldg(job.sw + kb + 1);
             }
-            const int buf = ib % C::kBufs;
-            if (!(ok = warp_wait(&sm.acc_full[buf], (ib / C::kBufs) & 1))) break;
-            tc_fence_after();
             auto release = [&] {
               tc_fence_before();
               __syncwarp();
@@ -480,15 +489,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (job.rows > 0) {
               const uint32_t t = t_lane + buf * BN;
+              constexpr int kStep = C::kStep;
 #pragma unroll
-              for (int c = 0; c < C::kCols; c += 32) {
-                uint32_t v[2][16];
-                TC_LD16(t + c, v[0]);
-                TC_LD16(t + c + 16, v[1]);
+              for (int c = 0; c < C::kCols; c += kStep) {
+                uint32_t v[kStep / 16][16];
+#pragma unroll
+                for (int j = 0; j < kStep / 16; ++j) TC_LD16(t + c + 16 * j, v[j]);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                if (c + 32 >= C::kCols) release();
+                if (c + kStep >= C::kCols) release();
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
+                for (int j = 0; j < kStep / 2; ++j)
                   acc[c / 2 + j] = fma2(pack2(v[j / 8][2 * (j % 8)], v[j / 8][2 * (j % 8) + 1]), s2, acc[c / 2 + j]);
               }
             } else {
@@ -629,19 +639,21 @@ cudaError_t launch_block_fp8_matmul(const BlockFp8Args& a, cudaStream_t st) {
   cudaError_t e = current_sm_count(&n_sm);
   if (e != cudaSuccess) return e;
   // Up to 16 rows on at most one tile per SM quantize themselves: one launch instead of two (a call
-  // of M = 1, N = K = 256 takes 7.3 instead of 10.7 us, M = 8, N = K = 4096 15 instead of 16 us; 32
-  // such rows 17 instead of 16 us, and where the matrices stream through every SM, 80 rows over 512
-  // of them, 36 instead of 34 us).
+  // of M = 1, N = K = 256 takes 7.3 instead of 9.5 us, M = 8, N = K = 4096 13.5 as with two; 32 such rows
+  // 17 instead of 14 us, and where the matrices stream through every SM, 80 rows over 512 of them, 36
+  // instead of 34 us).
   const int64_t few = std::min<int64_t>(a.M, a.G);   // tiles of rows, at most
   if (a.M <= 16 && few * ((a.N + 127) / 128) <= n_sm)
     return few * ((a.N + 63) / 64) <= n_sm ? launch_tile<64, kFused>(a, n_sm, st) : launch_tile<128, kFused>(a, n_sm, st);
   if ((e = launch_quantize_rows_block(a.x, a.M, a.K, a.x_codes, a.x_scales, st)) != cudaSuccess) return e;
   // Tiles of 128 x 256, at most one partial one per group.  Half as wide while half of the SMs would
-  // have none (M = 512, N = K = 4096: 24 against 28 us; M = 1024: 37 against 30 us); pairs of CTAs,
+  // have none (M = 512, N = K = 4096: 24 against 28 us; M = 1024: 37 against 30 us), a quarter while these
+  // fill the SMs once at most (M = 64, N = K = 4096: 13.7 against 15.0 us); pairs of CTAs,
   // which read a third less from L2, where groups fill their 256 rows and K is long enough for the
   // pair's start (N = K = 4096: 75 against 80 us at M = 4096; 640 rows per group, N = 2048: 624
   // against 608 us at K = 512).
   const int64_t row_tiles = a.G == 1 ? (a.M + kRows - 1) / kRows : a.M / kRows + std::min(a.M, a.G);
+  if (row_tiles * ((a.N + 63) / 64) <= n_sm) return launch_tile<64, kSingle>(a, n_sm, st);
   if (2 * row_tiles * ((a.N + 255) / 256) <= n_sm) return launch_tile<128, kSingle>(a, n_sm, st);
   if (a.M >= 256 * static_cast<int64_t>(a.G) && a.K >= 1024) return launch_tile<256, kPair>(a, n_sm, st);
   return launch_tile<256, kSingle>(a, n_sm, st);
