@@ -495,11 +495,11 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const float* __restri
   }
 }
 
-// Units per thread: one for rows of up to this many units, else two.  A row's sums cost a thread
+// Units per thread, forward: one for rows of up to this many units, else two.  A row's sums cost a thread
 // about as many instructions as a unit's arithmetic, and the kernels are bound by their instructions
 // and latencies before HBM: `after` with the next norm of 32768 x 2048 takes 115 us with one unit and
-// 87 us with two, the gradient of `before` of 16384 x 2048 56 and 47 us (2999 x 1000: 11 and 15 us).
-constexpr int kForwardOneUnit = 32, kBeforeGradOneUnit = 128;
+// 87 us with two, the gradient of `before` of 16384 x 2048 56 and 47 us.
+constexpr int kForwardOneUnit = 32;
 constexpr int kForwardThreads = 256;
 constexpr int kMaxSms = 160;     // the workspace holds the column sums of this many CTAs
 
@@ -538,6 +538,11 @@ NormLaunch grad_launch(int64_t T, int x, int threads, int n_sm) {
   return l;
 }
 
+// One unit per thread in the gradient of `before`: small rows, and few (1500 x 2048: 6.9 against 7.7 us,
+// 3000 x 2048 14.3 against 13.4).  With two, fp32 rows need 168 registers (384 threads; 16384 x 2048: 72 us,
+// with 128 registers 89).
+bool before_grad_one_unit(int64_t T, int units, int n_sm) { return units <= 128 || (units <= 256 && T < 16 * n_sm); }
+
 // Units per thread of the gradient of `after` (one: 512 threads, two or three: 384).  Two pay off once the
 // groups, of 1.5 times the rows in flight, have several rows each (16384 x 2048: 73 against 78 us,
 // 608 x 2048 8.2 against 7.2, 608 x 1280 6.5 against 7.0), and where one unit leaves an SM a single
@@ -568,7 +573,7 @@ NormArgs args_of(const moe_norm_t& s) {
 // columns) 64, some of them spilled in the latter.
 #define PICK_FORWARD(one, two, wide, more) (s.H / 8 <= kForwardOneUnit ? one : s.H / 8 <= 512 ? two : s.H / 8 <= 1024 ? wide : more)
 #define PICK_BEFORE(K, R) PICK_FORWARD((K<R, 1, 256, 4>), (K<R, 2, 256, 4>), (K<R, 2, 512, 2>), (K<R, 2, 1024, 1>))
-#define PICK_GRAD(K, R) (s.H / 8 <= kBeforeGradOneUnit ? K<R, 1, 512> : s.H / 8 <= 1024 ? K<R, 2, 512> : K<R, 2, 1024>)
+#define PICK_GRAD(K, R, threads) (one ? K<R, 1, 512> : a.units <= threads * 2 ? K<R, 2, threads> : a.units <= 1024 ? K<R, 2, 512> : K<R, 2, 1024>)
 #define PICK_AFTER_GATE(K, R, Y, element, next)                                                \
   PICK_FORWARD((K<R, Y, 1, 256, 2, element, next>), (K<R, Y, 2, 256, 2, element, next>), (K<R, Y, 2, 512, 1, element, next>), \
                (K<R, Y, 2, 1024, 1, element, next>))
@@ -636,9 +641,11 @@ cudaError_t launch_norm_before_grad(const moe_norm_t& s, const void* dn, const v
   a.dres = dres;
   a.dx = dx;
   a.part = part;
-  const NormLaunch l = grad_launch(s.T, row_threads(a.units, kBeforeGradOneUnit, true), kGradThreads, n_sm);
+  const bool one = before_grad_one_unit(s.T, a.units, n_sm);
+  const int threads = one || !s.residual_fp32 || a.units > 768 ? kGradThreads : 384;
+  const NormLaunch l = grad_launch(s.T, row_threads(a.units, one ? a.units : 0, true), threads, n_sm);
   const int grid = static_cast<int>(l.grid.x);
-  auto kern = s.residual_fp32 ? PICK_GRAD(norm_before_grad_kernel, float) : PICK_GRAD(norm_before_grad_kernel, uint16_t);
+  auto kern = s.residual_fp32 ? PICK_GRAD(norm_before_grad_kernel, float, 384) : PICK_GRAD(norm_before_grad_kernel, uint16_t, 512);
   e = launch_pdl(true, kern, l.grid, l.block, 0, st, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(true, norm_columns_kernel, dim3((s.H + 31) / 32, 1), dim3(256), 0, st,

@@ -18,6 +18,7 @@ CASES = [
     (701, 1288, BF, BF, "channel", True, 0.0), (650, 2080, FP, FP, "token", True, 1.0), (37, 2504, BF, FP, "channel", True, 0.0),
     (161, 3200, BF, BF, "element", True, 0.0), (21, 4608, FP, FP, "element", True, 0.0), (170, 776, FP, BF, "element", True, 1.0),
     (9, 6152, BF, BF, "channel", True, 0.0), (6, 9208, FP, FP, "element", True, 0.0), (5, 9224, BF, BF, "element", True, 1.0),
+    (2500, 1096, FP, BF, "none", False, 0.0), (2501, 1288, BF, BF, "none", True, 0.0),
 ]
 IDS = lambda c: f"T{c[0]}_H{c[1]}_{c[4]}{'_next' if c[5] else ''}"  # noqa: E731
 
