@@ -16,6 +16,8 @@
 // before the current one's sums, whose barriers it would otherwise wait behind.  Sums are fp32 in a fixed
 // order: a row's by shuffles and one array per group, a column's in registers over the group's
 // rows, then over the CTA's groups, written per CTA and summed by a second kernel (no atomics).
+// 32768 x 2048 bf16: before 43 us, after with the next norm 87 (6.2 TB/s); gradients of 16384 x 2048: before
+// 47, after with the next norm 73 us (5.5 TB/s); 8 rows take 1.7 to 4.3 us.
 #include <algorithm>
 
 #include "row_units.cuh"

@@ -9,7 +9,9 @@
 //   return   out[t] = sum_j w[s] ys[p(s)]           return'  dys[p(s)] = w[s] dout[t],
 //                                                            dw[s] = <dout[t], ys[p(s)]>
 // with sums over the routed ranks only, in fp32 and in rank order (no atomics: the same bits on
-// every call).  All four move S rows once and T rows once and are bound by HBM.
+// every call).  All four move S rows once and T rows once (return' S rows twice) and are bound by HBM:
+// 32768 x 2048 bf16, k = 10, E = 512: sort 234 us, return and sort' 235 (6.3 TB/s), return' 430 (6.6);
+// 4096 such tokens: 37, 33 and 58 us, of which the sort counts and places for 8.
 #include <algorithm>
 
 #include "internal.cuh"
