@@ -21,7 +21,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxChunks = 64;               // CTAs of the counting sort, a run of slots each
+// CTAs of the counting sort, a run of slots each.  The sort of 4096 x 2048, k = 10 takes 37.7 us; with runs of
+// 512 slots and up to 128 CTAs, whose counts every CTA adds up, 40.8, with runs of 2048 39.5.
+constexpr int kMaxChunks = 64;
 constexpr int kMinChunk = 1024;
 constexpr int kSortThreads = 1024;
 constexpr int kPlaceWarps = 16;              // warps that place a chunk's slots
